@@ -438,6 +438,117 @@ KVC_API kvc_status kvc_attend_paged_noalloc(const void* q_dev, void* o_dev, cons
                                             int32_t num_heads, int32_t head_dim, int32_t page_size,
                                             float softmax_scale, int32_t kv_splits, void* stream);
 
+/* ---- A batch of sequences over one page pool: append, attention that reads a shared prefix
+ * once, the attention weight that every cached token receives, and eviction by that weight.
+ * Streams that share their first frames, or a server's answers behind one instruction, in
+ * caches that are bounded per sequence and KV head. The pages describe attention-weight
+ * pruning as the alternative that fast attention kernels leave out because they do not
+ * build the weights ([IVG] Building Blocks); here a second pass over the keys computes them.
+ *
+ * The caller owns every buffer (device memory of the current device) and describes them in
+ * a kvc_paged_batch; calls read the struct before they return, allocate nothing, enqueue
+ * their work on `stream` and never wait, so they can be captured into a CUDA graph, which
+ * then follows the lengths, rows and tables that the buffers hold when it runs. Calls that
+ * may run at the same time need different workspaces, and none may run while another
+ * writes the buffers that it reads.
+ *
+ * Pages are laid out as kvc_append_frame writes them, [page][KV head][slot][dim], and a
+ * sequence's page that kvc_paged_append began or kvc_paged_evict cut ends in zeros, so the
+ * pages can be given to kvc_attend_paged_noalloc (16-slot pages, 64 dims, bf16, as many
+ * query heads as KV heads). No page may be in two sequences' rows of the page table, or in
+ * the prefix and a row, if it is appended to or evicted from.
+ *
+ * Query head i reads KV head i / (num_q_heads / num_kv_heads). Rows of Q, K and V are the
+ * sequences' tokens one after another: row_start_dev[b] <= row < row_start_dev[b + 1] are
+ * sequence b's; rows outside [row_start_dev[0], row_start_dev[num_seqs]) are neither read nor
+ * written. Row strides are in elements (a slice of a fused QKV tensor can be given), rows
+ * 16-byte aligned.
+ *
+ * What the host cannot see is checked on the device: lengths and rows outside their buffers
+ * are taken as the nearest that are inside, a page outside the pool is skipped (its keys and
+ * values count as zeros; nothing is written to it), and the error word is set. */
+typedef struct {
+  int32_t dtype;                /* KVC_F32 or KVC_BF16: Q, K, V, O and the pools */
+  int32_t num_seqs;             /* sequences, 1 to 65,535 */
+  int32_t num_q_heads;          /* a multiple of num_kv_heads, at most 64 times it */
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128 */
+  int32_t page_size;            /* slots per page: 16, 32, 64, 128 or 256 */
+  int32_t max_pages;            /* columns of page_table; a sequence holds max_pages * page_size tokens at most */
+  int32_t prefix_tokens;        /* tokens of the shared prefix; 0: none */
+  int64_t pool_pages;           /* pages of each pool; pool_pages * num_kv_heads * page_size < 2^31 */
+  void* k_pool;                 /* [pool_pages][num_kv_heads][page_size][head_dim], 16-byte aligned */
+  void* v_pool;
+  const int32_t* page_table;    /* [num_seqs][max_pages] pages of each sequence's own tokens */
+  int32_t* lengths;             /* [num_seqs] tokens that each sequence holds (without the prefix) */
+  const int32_t* prefix_pages;  /* [ceil(prefix_tokens / page_size)] or NULL */
+  int32_t* next_positions;      /* [num_seqs] position of the next token appended, or NULL */
+  float* scores;                /* [num_seqs][num_kv_heads][max_pages * page_size] accumulated weight
+                                   of the token in each slot, or NULL */
+  int32_t* positions;           /* same shape: position of the token in each slot, or NULL */
+  int32_t* error;               /* one word, or NULL: set from 0 by the first device-side failure: 1 a
+                                   bounded wait gave up, 2 no room for an append, 3 a length, row
+                                   or page out of range */
+  float softmax_scale;
+  int32_t reserved;             /* must be zero */
+} kvc_paged_batch;
+
+/* Bytes of workspace (256-byte aligned device memory is best, 16 is enough) that the calls
+ * below need on the current device for up to `rows` rows of Q and, for kvc_paged_evict, this
+ * `keep` (0: no eviction). Nothing in it needs to start at zero or to survive between calls.
+ * Errors: KVC_ERR_ARG (a batch that no call would take, negative counts), KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t rows, int32_t keep,
+                                       int64_t* bytes_out);
+
+/* Append each sequence's rows of k_dev and v_dev [rows, num_kv_heads, head_dim] to its pages,
+ * in the slots from lengths[b] on; set their scores to 0 and their positions to
+ * next_positions[b], next_positions[b] + 1, ... (each where the batch has that array), and
+ * clear the rest of a page that is begun. Then lengths[b] and next_positions[b] grow by the
+ * sequence's rows. A sequence whose rows do not fit takes none of them (error word 2).
+ * Errors: KVC_ERR_ARG (batch, pointers, strides; positions without next_positions),
+ * KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void* k_dev, const void* v_dev,
+                                    int64_t k_row_stride, int64_t v_row_stride, int32_t rows,
+                                    const int32_t* row_start_dev, void* stream);
+
+/* Attention of q_dev [rows, num_q_heads, head_dim] over the prefix and each sequence's own
+ * tokens: O_i = sum_j softmax_j(softmax_scale q_i . k_j) v_j, and lse_dev [rows, num_q_heads]
+ * (fp32, may be NULL) the natural logarithm of sum_j e^(softmax_scale q_i . k_j). With
+ * causal = 1 the rows are the sequence's last n tokens (appended before the call): row i of n
+ * sees the prefix and the slots up to lengths[b] - n + i; with 0 it sees every slot. A row
+ * that sees nothing gets O = 0 and an LSE of -inf. The prefix's keys and values are read for
+ * the whole batch at once. o_dev is densely packed. bf16 runs on tcgen05 tensor cores (fp32
+ * logits, statistics and accumulation, weights rounded to bf16 for the second product), fp32
+ * in fp32 arithmetic. Logits are to stay below 2^20 in magnitude, as for kvc_attend.
+ * Errors: KVC_ERR_ARG (batch, pointers, strides, more than 2^32 row-heads, a workspace
+ * that is too small), KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
+                                    void* o_dev, float* lse_dev, int32_t rows, const int32_t* row_start_dev,
+                                    int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* The attention weight that each of a sequence's own tokens receives, added to its score:
+ * scores[b][h][j] += sum over the sequence's rows i and the query heads of KV head h of
+ * e^(softmax_scale q_i . k_j - lse_i), over the rows that see slot j (`causal` as in
+ * kvc_paged_attend, whose q_dev and lse_dev these are; another LSE, e.g. over a window of
+ * keys, is as good). The sums are fp32, in an order that depends on the sizes alone. A
+ * row with an LSE of +inf adds nothing. Errors: as kvc_paged_attend; KVC_ERR_ARG without
+ * scores. */
+KVC_API kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
+                                     const float* lse_dev, int32_t rows, const int32_t* row_start_dev,
+                                     int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Cut every sequence that holds more than `keep` tokens to `keep`, each KV head its own: kept
+ * are the tokens at positions below `sinks`, those at positions from next_positions[b] - recent
+ * on, and then those of highest score (ties: the lower slot; a NaN counts as lowest). Kept
+ * tokens in the first `keep` slots stay in place; the others move, in ascending slot, into the
+ * evicted tokens' slots, in ascending slot, with K, V, score and position. The last kept page
+ * ends in zeros; later pages, and scores and positions past the length, are left as they
+ * were. Then lengths[b] = keep. sinks + recent must not pass `keep`, and a sequence holds at
+ * most 393,216 slots. Errors: KVC_ERR_ARG (batch, no scores, positions or next_positions,
+ * counts, workspace), KVC_ERR_UNSUPPORTED (more slots), KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_paged_evict(const kvc_paged_batch* batch, int32_t keep, int32_t sinks, int32_t recent,
+                                   void* workspace_dev, int64_t workspace_bytes, void* stream);
+
 /* Test hooks for failure handling, tested without any GPU fault:
  *   kvc_debug_fail_allocs(n): the n-th next device allocation inside
  *     kvc_create reports failure (n = 0 disables), which must surface as

@@ -31,7 +31,8 @@ EXPORTS = ["kvc_create", "kvc_destroy", "kvc_set_stream", "kvc_reset", "kvc_appe
            "kvc_debug_fail_allocs", "kvc_debug_bounded_wait", "kvc_attend_paged_noalloc", "kvc_append_frame_all",
            "kvc_step_host_async", "kvc_set_layer_budgets", "kvc_prune", "kvc_layer_diversity",
            "kvc_head_tokens", "kvc_scale_phase", "kvc_export_fp8_group_scales", "kvc_last_raw_scores",
-           "kvc_adapt_layer_budgets"]
+           "kvc_adapt_layer_budgets", "kvc_paged_workspace", "kvc_paged_append", "kvc_paged_attend",
+           "kvc_paged_weights", "kvc_paged_evict"]
 
 
 class kvc_config(ctypes.Structure):
@@ -56,6 +57,17 @@ class kvc_info(ctypes.Structure):
 
     def as_dict(self):
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
+
+
+class kvc_paged_batch(ctypes.Structure):
+    """include/kvc.h's struct of a paged batch; make_paged_batch fills it from tensors."""
+    _fields_ = [("dtype", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("prefix_tokens", ctypes.c_int32), ("pool_pages", ctypes.c_int64),
+                ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p), ("next_positions", ctypes.c_void_p),
+                ("scores", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("error", ctypes.c_void_p),
+                ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class KVCError(RuntimeError):
@@ -105,6 +117,14 @@ def _load():
         "kvc_debug_bounded_wait": ([vp, i32], i32),
         "kvc_attend_paged_noalloc": ([vp, vp, vp, vp, ctypes.c_int64, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                       i32, vp], i32),
+        "kvc_paged_workspace": ([ctypes.POINTER(kvc_paged_batch), i32, i32, i64p], i32),
+        "kvc_paged_append": ([ctypes.POINTER(kvc_paged_batch), vp, vp, ctypes.c_int64, ctypes.c_int64, i32, vp, vp],
+                             i32),
+        "kvc_paged_attend": ([ctypes.POINTER(kvc_paged_batch), vp, ctypes.c_int64, vp, vp, i32, vp, i32, vp,
+                              ctypes.c_int64, vp], i32),
+        "kvc_paged_weights": ([ctypes.POINTER(kvc_paged_batch), vp, ctypes.c_int64, vp, i32, vp, i32, vp,
+                               ctypes.c_int64, vp], i32),
+        "kvc_paged_evict": ([ctypes.POINTER(kvc_paged_batch), i32, i32, i32, vp, ctypes.c_int64, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -402,6 +422,156 @@ def kvc_attend_paged_noalloc(q, o, k_pool, v_pool, pool_pages: int, page_table, 
                                        _stream(stream))
     if st != 0:
         raise KVCError(st, "kvc_attend_paged_noalloc failed")
+
+
+# ---------------------------------------------------------------- paged batches
+
+def _same_device(what, x, device, dtype=None, shape=None):
+    """A CUDA tensor of the batch's device (and type and shape), packed densely."""
+    if not getattr(x, "is_cuda", False):
+        raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
+    if x.device != device:
+        raise ValueError(f"{what} is on {x.device}, the batch on {device}")
+    if dtype is not None and x.dtype != dtype:
+        raise TypeError(f"{what} is {x.dtype}, not {dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(x.shape)}, not {tuple(shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return x
+
+
+def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, softmax_scale: float, *,
+                     prefix_pages=None, prefix_tokens: int = 0, next_positions=None, scores=None, positions=None,
+                     error=None) -> kvc_paged_batch:
+    """A batch over caller-owned tensors: pools [pages, KV heads, page size, head dim] (fp32 or
+    bf16), page_table int32 [sequences, pages of each], and the other arrays of include/kvc.h's
+    struct. The struct keeps the tensors alive; the calls below read and write them in place."""
+    import torch
+    types = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}
+    dev, i32 = k_pool.device, torch.int32
+    if k_pool.dtype not in types or k_pool.dim() != 4:
+        raise TypeError("k_pool must be a 4-dimensional float32 or bfloat16 tensor")
+    _same_device("k_pool", k_pool, dev)
+    _same_device("v_pool", v_pool, dev, k_pool.dtype, k_pool.shape)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [sequences, pages]")
+    n, max_pages = page_table.shape
+    pool_pages, heads, page, dim = k_pool.shape
+    _same_device("page_table", page_table, dev, i32)
+    _same_device("lengths", lengths, dev, i32, (n,))
+    if prefix_pages is not None:
+        _same_device("prefix_pages", prefix_pages, dev, i32)
+    if prefix_tokens > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_tokens):
+        raise ValueError("prefix_pages must hold prefix_tokens tokens")
+    if next_positions is not None:
+        _same_device("next_positions", next_positions, dev, i32, (n,))
+    if scores is not None:
+        _same_device("scores", scores, dev, torch.float32, (n, heads, max_pages * page))
+    if positions is not None:
+        _same_device("positions", positions, dev, i32, (n, heads, max_pages * page))
+    if error is not None:
+        _same_device("error", error, dev, i32)
+        if error.numel() < 1:
+            raise ValueError("error must hold one word")
+    b = kvc_paged_batch()
+    b.dtype, b.num_seqs, b.num_q_heads, b.num_kv_heads = types[k_pool.dtype], n, num_q_heads, heads
+    b.head_dim, b.page_size, b.max_pages, b.prefix_tokens = dim, page, max_pages, prefix_tokens
+    b.pool_pages, b.softmax_scale = pool_pages, softmax_scale
+    held = dict(k_pool=k_pool, v_pool=v_pool, page_table=page_table, lengths=lengths, prefix_pages=prefix_pages,
+                next_positions=next_positions, scores=scores, positions=positions, error=error)
+    for name, x in held.items():
+        setattr(b, name, None if x is None else x.data_ptr())
+    b._tensors, b._device, b._dtype = held, dev, k_pool.dtype
+    return b
+
+
+def _paged_rows(batch, what, x, heads):
+    """(pointer, row stride, rows) of a [rows, heads, head dim] tensor whose rows are packed."""
+    if not getattr(x, "is_cuda", False):
+        raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
+    if x.device != batch._device or x.dtype != batch._dtype:
+        raise ValueError(f"{what} is {x.dtype} on {x.device}, the batch {batch._dtype} on {batch._device}")
+    d = batch.head_dim
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or x.stride(2) != 1 or \
+            (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{what} must be [rows, {heads}, {d}] with packed rows")
+    rows = x.shape[0]
+    return x.data_ptr(), (x.stride(0) if rows > 1 else heads * d), rows
+
+
+def _paged_call(batch, stream, fn, *args):
+    """fn(batch, *args, stream) with the batch's device current; the default stream is that
+    device's current one."""
+    import torch
+    if torch.cuda.current_device() == batch._device.index:
+        st = fn(ctypes.byref(batch), *args, _stream(stream))
+    else:
+        with torch.cuda.device(batch._device):
+            st = fn(ctypes.byref(batch), *args, _stream(stream))
+    if st != 0:
+        raise KVCError(st, f"{fn.__name__} failed")
+
+
+def _row_start(batch, x):
+    import torch
+    return _same_device("row_start", x, batch._device, torch.int32, (batch.num_seqs + 1,)).data_ptr()
+
+
+def _workspace(batch, x):
+    _same_device("workspace", x, batch._device)
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
+def kvc_paged_workspace(batch: kvc_paged_batch, rows: int, keep: int = 0) -> int:
+    """Bytes of workspace for calls with up to `rows` rows and an eviction to `keep`."""
+    import torch
+    n = ctypes.c_int64(0)
+    with torch.cuda.device(batch._device):
+        st = _lib.kvc_paged_workspace(ctypes.byref(batch), rows, keep, ctypes.byref(n))
+    if st != 0:
+        raise KVCError(st, "kvc_paged_workspace failed")
+    return n.value
+
+
+def kvc_paged_append(batch: kvc_paged_batch, k, v, row_start, stream=None) -> None:
+    """Append k, v [rows, KV heads, head dim] (rows row_start[b] .. of sequence b)."""
+    kp, ks, rows = _paged_rows(batch, "k", k, batch.num_kv_heads)
+    vp, vs, v_rows = _paged_rows(batch, "v", v, batch.num_kv_heads)
+    if rows != v_rows:
+        raise ValueError("k and v have different numbers of rows")
+    _paged_call(batch, stream, _lib.kvc_paged_append, kp, vp, ks, vs, rows, _row_start(batch, row_start))
+
+
+def kvc_paged_attend(batch: kvc_paged_batch, q, o, row_start, workspace, lse=None, causal: bool = True,
+                     stream=None) -> None:
+    """Attention of q [rows, query heads, head dim] into o (and the log-sum-exp into lse
+    [rows, query heads] fp32) over the shared prefix and the sequences' own tokens."""
+    import torch
+    qp, qs, rows = _paged_rows(batch, "q", q, batch.num_q_heads)
+    _same_device("o", o, batch._device, batch._dtype, q.shape)
+    if lse is not None:
+        _same_device("lse", lse, batch._device, torch.float32, q.shape[:2])
+    wp, wn = _workspace(batch, workspace)
+    _paged_call(batch, stream, _lib.kvc_paged_attend, qp, qs, o.data_ptr(),
+                None if lse is None else lse.data_ptr(), rows, _row_start(batch, row_start), int(bool(causal)), wp, wn)
+
+
+def kvc_paged_weights(batch: kvc_paged_batch, q, lse, row_start, workspace, causal: bool = True,
+                      stream=None) -> None:
+    """Add the attention weight that each of the sequences' own tokens receives to its score."""
+    import torch
+    qp, qs, rows = _paged_rows(batch, "q", q, batch.num_q_heads)
+    _same_device("lse", lse, batch._device, torch.float32, q.shape[:2])
+    wp, wn = _workspace(batch, workspace)
+    _paged_call(batch, stream, _lib.kvc_paged_weights, qp, qs, lse.data_ptr(), rows, _row_start(batch, row_start),
+                int(bool(causal)), wp, wn)
+
+
+def kvc_paged_evict(batch: kvc_paged_batch, keep: int, sinks: int, recent: int, workspace, stream=None) -> None:
+    """Cut every sequence to its `keep` tokens: sinks, recent ones, then the highest scores."""
+    wp, wn = _workspace(batch, workspace)
+    _paged_call(batch, stream, _lib.kvc_paged_evict, keep, sinks, recent, wp, wn)
 
 
 @dataclass

@@ -1,0 +1,475 @@
+// kvc_paged.cu -- the paged-batch entry points (kvc_paged_*): argument checks, workspace,
+// the append and the merge of partial attention results.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "kvc_paged.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kMaxGroup = 64;                  // query heads per KV head
+constexpr long long kMaxSlots = 1LL << 30;     // slots of a sequence, tokens of the prefix
+
+bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
+
+bool valid_batch(const kvc_paged_batch* b) {
+  if (!b) return false;
+  if (b->dtype != KVC_F32 && b->dtype != KVC_BF16) return false;
+  if (b->head_dim != 64 && b->head_dim != 128) return false;
+  const int P = b->page_size;
+  if (P < 16 || P > 256 || (P & (P - 1))) return false;
+  if (b->num_seqs < 1 || b->num_seqs > 65535 || b->num_kv_heads < 1 || b->num_q_heads < 1 ||
+      b->num_q_heads > 65535 || b->num_q_heads % b->num_kv_heads || b->num_q_heads / b->num_kv_heads > kMaxGroup)
+    return false;
+  if (b->max_pages < 1 || b->max_pages > kMaxSlots / P || b->pool_pages < 1) return false;
+  // pool rows (pages x heads x slots) index the tensor maps as int
+  if (b->pool_pages > INT_MAX / (static_cast<long long>(b->num_kv_heads) * P)) return false;
+  if (b->prefix_tokens < 0 || b->prefix_tokens > kMaxSlots || (b->prefix_tokens > 0 && !b->prefix_pages)) return false;
+  if (!(b->softmax_scale > 0.f) || !std::isfinite(b->softmax_scale) || b->reserved != 0) return false;
+  if (!b->k_pool || !b->v_pool || !b->page_table || !b->lengths) return false;
+  return aligned16(b->k_pool) && aligned16(b->v_pool);
+}
+
+int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+bool valid_rows(const kvc_paged_batch* b, const void* x, long long stride, int heads, int32_t rows) {
+  if (rows < 0 || !aligned16(x) || (rows > 0 && !x)) return false;
+  const int per16 = b->dtype == KVC_F32 ? 4 : 8;
+  return stride >= static_cast<long long>(heads) * b->head_dim && stride % per16 == 0 && stride <= (1LL << 36);
+}
+
+// ------------------------------------------------------------------ the schedule and its workspace
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Layout {
+  size_t plan, part_o, part_ml, part_w, part_id, bytes;
+};
+
+PagedParams base_params(const kvc_paged_batch* b, int32_t rows, const int32_t* row_start, int sms) {
+  PagedParams p{};
+  p.B = b->num_seqs;
+  p.Hq = b->num_q_heads;
+  p.Hkv = b->num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.D = b->head_dim;
+  p.page_shift = page_shift(b->page_size);
+  p.max_pages = b->max_pages;
+  p.rows = rows;
+  p.pool_pages = b->pool_pages;
+  p.page_table = b->page_table;
+  p.lengths = b->lengths;
+  p.prefix_pages = b->prefix_pages;
+  p.row_start = row_start;
+  p.k_pool = b->k_pool;
+  p.v_pool = b->v_pool;
+  p.scale_log2 = b->softmax_scale * 1.4426950408889634f;
+  p.err = b->error;
+  p.grid = sms;
+  return p;
+}
+
+void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
+  p->prefix_tokens = b->prefix_tokens;
+  // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend
+  // its products on padding), else of 64
+  const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
+  p->slot_rows = per_seq <= 16 ? 16 : 64;
+  p->tile_tokens = p->item_tokens = p->slot_rows / p->G;
+  p->key_tile = 64;
+  p->streams = 1;
+  p->grid *= 2;
+}
+
+void weights_schedule(PagedParams* p) {
+  p->prefix_tokens = 0;                        // the prefix keeps no scores
+  const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
+  p->tile_tokens = p->item_tokens = (per_seq <= 16 ? 16 : 64) / p->G;
+  p->key_tile = 64;
+  p->streams = 1;
+  p->slot_rows = p->key_tile;
+  p->grid *= 2;
+}
+
+Layout attend_layout(const PagedParams& p) {
+  Layout l{};
+  const size_t slots = static_cast<size_t>(row_slots(p.rows, p.Hq, p.streams, p.prefix_tokens > 0)) +
+                       static_cast<size_t>(p.grid) * p.slot_rows;
+  l.plan = 0;
+  l.part_ml = align256(8 * (static_cast<size_t>(p.B) + 1));
+  l.part_o = l.part_ml + align256(slots * sizeof(float2));
+  l.bytes = l.part_o + align256(slots * p.D * sizeof(float));
+  return l;
+}
+
+Layout weights_layout(const PagedParams& p) {
+  Layout l{};
+  l.plan = 0;
+  l.part_id = align256(8 * (static_cast<size_t>(p.B) + 1));
+  l.part_w = l.part_id + align256(static_cast<size_t>(p.grid) * sizeof(int4));
+  l.bytes = l.part_w + align256(static_cast<size_t>(p.grid) * p.slot_rows * sizeof(float));
+  return l;
+}
+
+int move_cap(const kvc_paged_batch* b, int32_t keep) {
+  const long long cap = static_cast<long long>(b->max_pages) * b->page_size;
+  return static_cast<int>(std::min<long long>(keep, std::max<long long>(cap - keep, 0)));
+}
+size_t evict_bytes(const kvc_paged_batch* b, int32_t keep) {
+  return align256(sizeof(int32_t) * 2 * static_cast<size_t>(b->num_seqs) * b->num_kv_heads * move_cap(b, keep));
+}
+
+// ------------------------------------------------------------------ append
+struct AppendParams {
+  int B, H, page_shift, max_pages, rows, row_bytes;   // row_bytes: one head's
+  long long pool_pages, k_stride, v_stride;           // bytes between source rows
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* next_positions;
+  const int32_t* row_start;
+  const uint8_t* k;
+  const uint8_t* v;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* scores;
+  int32_t* positions;
+  int* err;
+};
+
+// One warp per row, and per slot behind a sequence's last token that may need clearing: a page
+// that this call begins ends in zeros, as every page of the cache does. Bound by the copies
+// (rows in, slots out); 16 bytes a lane.
+__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  const int page_size = 1 << p.page_shift;
+  int b, slot = 0, row = -1;
+  if (warp < p.rows) {
+    b = find_sequence(p.row_start, p.B, warp);
+    row = warp;
+  } else {
+    const int z = warp - p.rows;
+    b = z / (page_size - 1);
+    slot = z % (page_size - 1);
+    if (b >= p.B) return;
+  }
+  if (b < 0) return;                                   // behind the last sequence
+  const int lo = p.row_start[b], hi = p.row_start[b + 1], len = p.lengths[b];
+  const int cap = p.max_pages << p.page_shift;
+  if (lo < 0 || hi < lo || hi > p.rows || len < 0 || len > cap) {
+    if (lane == 0) latch_error(p.err, DERR_BOUNDS);
+    return;
+  }
+  const int n = hi - lo;
+  if (n > cap - len) {                                 // no room: none of the sequence's rows
+    if (lane == 0) latch_error(p.err, DERR_POOL);
+    return;
+  }
+  if (row >= 0) {
+    slot = len + row - lo;
+  } else {
+    const int end = len + n;
+    const int first = end & ~(page_size - 1);          // first slot of the last page written
+    slot += end;
+    if (n == 0 || end == first || first < len || slot >= first + page_size) return;
+  }
+  const int32_t page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + (slot >> p.page_shift));
+  if (page < 0 || page >= p.pool_pages) {
+    if (lane == 0) latch_error(p.err, DERR_BOUNDS);
+    return;
+  }
+  const int per_head = p.row_bytes >> 4, chunks = p.H * per_head;
+  const long long head_bytes = static_cast<long long>(p.row_bytes) << p.page_shift;
+  const long long base = page * p.H * head_bytes + (slot & (page_size - 1)) * static_cast<long long>(p.row_bytes);
+  const uint4* k = reinterpret_cast<const uint4*>(p.k + (row >= 0 ? row * p.k_stride : 0));
+  const uint4* v = reinterpret_cast<const uint4*>(p.v + (row >= 0 ? row * p.v_stride : 0));
+  for (int c = lane; c < chunks; c += 32) {
+    const long long to = base + (c / per_head) * head_bytes + (c % per_head) * 16;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(p.k_pool + to) = row >= 0 ? __ldg(k + c) : zero;
+    *reinterpret_cast<uint4*>(p.v_pool + to) = row >= 0 ? __ldg(v + c) : zero;
+  }
+  if (row < 0) return;
+  for (int h = lane; h < p.H; h += 32) {
+    const long long at = (static_cast<long long>(b) * p.H + h) * cap + slot;
+    if (p.scores) p.scores[at] = 0.f;
+    if (p.positions) p.positions[at] = p.next_positions[b] + row - lo;
+  }
+}
+
+// Lengths and next positions of the sequences that were appended to.
+__global__ void paged_grow_kernel(const int32_t* row_start, int32_t* lengths, int32_t* next_positions, int B, int rows,
+                                  int cap) {
+  griddep_wait();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= B) return;
+  const int lo = row_start[b], hi = row_start[b + 1], len = lengths[b];
+  if (lo < 0 || hi < lo || hi > rows || len < 0 || len > cap || hi - lo > cap - len) return;
+  lengths[b] = len + hi - lo;
+  if (next_positions) next_positions[b] += hi - lo;
+}
+
+// ------------------------------------------------------------------ merging partial results
+// One warp per (row, query head): O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the row's
+// partials in the order of their keys, LSE = ln 2 (M + log2 of that sum). A row that sees no key
+// gets O = 0 and LSE = -inf.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int kPer = D / 32;
+  const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int row = static_cast<int>(warp / p.Hq), hq = static_cast<int>(warp % p.Hq);
+  if (row >= p.rows) return;
+  const int b = find_sequence(p.row_start, p.B, row);
+  if (b < 0) return;                                   // behind the last sequence: left as it was
+  const long long U = p.plan[0];
+  const int h = hq / p.G, g = hq % p.G;
+  float M = -INFINITY, L = 0.f, acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+  auto add = [&](long long slot) {
+    const float2 ml = p.part_ml[slot];
+    if (ml.y == 0.f) return;                           // saw none of its keys
+    const float m = fmaxf(M, ml.x);
+    const float f0 = exp2f(M - m), f1 = exp2f(ml.x - m);
+    M = m;
+    L = L * f0 + ml.y * f1;
+    const float* src = p.part_o + slot * D + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f0 + src[i] * f1;
+  };
+  for (int part = p.prefix_tokens > 0 ? 0 : 1; part < 2; ++part) {
+    const int s = part == 0 ? -1 : b;                  // the prefix's keys, then the sequence's own
+    const SeqView v = seq_view(p, s);
+    const int t = row - v.r0;
+    const int item = t / p.item_tokens, in = t - item * p.item_tokens;
+    const int nk = item_units(p, s, v, item);
+    if (nk > 0 && t >= 0 && t < v.n) {
+      const long long first = (s < 0 ? 0 : p.plan[1 + s]) + h * head_units(p, s, v) + units_before(p, s, v, item);
+      const bool split = p.streams == 2 && min(p.item_tokens, v.n - item * p.item_tokens) <= p.tile_tokens;
+      const int tile = in / p.tile_tokens;
+      const int r = (in - tile * p.tile_tokens) * p.G + g;
+      const int c0 = static_cast<int>(first / U), c1 = static_cast<int>((first + nk - 1) / U);
+      for (int c = c0; c <= c1; ++c)
+        for (int k = 0; k < (split ? 2 : 1); ++k)
+          add(c == c0 ? row_slot(p, s, k, row, hq)
+                      : cta_slot(p, c, (split ? k : tile) * (p.slot_rows / p.streams) + r));
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+  T* out = static_cast<T*>(p.o) + (static_cast<long long>(row) * p.Hq + hq) * D + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) out[i] = static_cast<T>(acc[i] * inv);
+  if (p.lse && lane == 0)
+    p.lse[static_cast<long long>(row) * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <typename T>
+cudaError_t launch_merge(cudaStream_t s, const PagedParams& p) {
+  const long long warps = static_cast<long long>(p.rows) * p.Hq;
+  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
+  return p.D == 64 ? launch_pdl(paged_merge_kernel<T, 64>, grid, dim3(128), 0, s, p)
+                   : launch_pdl(paged_merge_kernel<T, 128>, grid, dim3(128), 0, s, p);
+}
+
+// Weights of key blocks whose query tiles were split over CTAs: the run of continuing CTAs of a
+// key block is summed in order by the CTA that stands first in it.
+__global__ void __launch_bounds__(256) paged_weights_merge_kernel(const PagedParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = blockIdx.x;
+  const int4 id = p.part_id[c];
+  if (!id.w) return;
+  auto same = [&](int k) {
+    if (k < 0 || k >= p.grid) return false;
+    const int4 o = p.part_id[k];
+    return o.w && o.x == id.x && o.y == id.y && o.z == id.z;
+  };
+  if (same(c - 1)) return;
+  int end = c + 1;
+  while (same(end)) ++end;
+  const SeqView v = seq_view(p, id.x);
+  for (int i = threadIdx.x; i < p.key_tile; i += blockDim.x) {
+    const int key = id.z * p.key_tile + i;
+    if (key >= v.len) continue;
+    float sum = 0.f;
+    for (int k = c; k < end; ++k) sum += p.part_w[static_cast<long long>(k) * p.slot_rows + i];
+    p.scores[(static_cast<long long>(id.x) * p.Hkv + id.y) * paged_cap(p) + key] += sum;
+  }
+}
+
+kvc_status status_of(cudaError_t e) { return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA; }
+
+}  // namespace
+}  // namespace kvc
+
+extern "C" kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t rows, int32_t keep,
+                                          int64_t* bytes_out) {
+  using namespace kvc;
+  if (!bytes_out || !valid_batch(batch) || rows < 0 || keep < 0) return KVC_ERR_ARG;
+  const int sms = sm_count();
+  if (sms < 1) return KVC_ERR_CUDA;
+  size_t most = 256;
+  PagedParams p = base_params(batch, rows, nullptr, sms);
+  attend_schedule(&p, batch);
+  most = std::max(most, attend_layout(p).bytes);
+  p = base_params(batch, rows, nullptr, sms);
+  weights_schedule(&p);
+  most = std::max(most, weights_layout(p).bytes);
+  most = std::max(most, evict_bytes(batch, keep));
+  *bytes_out = static_cast<int64_t>(most);
+  return KVC_OK;
+}
+
+extern "C" kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void* k_dev, const void* v_dev,
+                                       int64_t k_row_stride, int64_t v_row_stride, int32_t rows,
+                                       const int32_t* row_start_dev, void* stream) {
+  using namespace kvc;
+  if (!valid_batch(batch) || !row_start_dev || !valid_rows(batch, k_dev, k_row_stride, batch->num_kv_heads, rows) ||
+      !valid_rows(batch, v_dev, v_row_stride, batch->num_kv_heads, rows) ||
+      (batch->positions && !batch->next_positions))
+    return KVC_ERR_ARG;
+  if (rows == 0) return KVC_OK;
+  const int elem = batch->dtype == KVC_F32 ? 4 : 2;
+  AppendParams p{};
+  p.B = batch->num_seqs;
+  p.H = batch->num_kv_heads;
+  p.page_shift = page_shift(batch->page_size);
+  p.max_pages = batch->max_pages;
+  p.rows = rows;
+  p.row_bytes = batch->head_dim * elem;
+  p.pool_pages = batch->pool_pages;
+  p.k_stride = k_row_stride * elem;
+  p.v_stride = v_row_stride * elem;
+  p.page_table = batch->page_table;
+  p.lengths = batch->lengths;
+  p.next_positions = batch->next_positions;
+  p.row_start = row_start_dev;
+  p.k = static_cast<const uint8_t*>(k_dev);
+  p.v = static_cast<const uint8_t*>(v_dev);
+  p.k_pool = static_cast<uint8_t*>(batch->k_pool);
+  p.v_pool = static_cast<uint8_t*>(batch->v_pool);
+  p.scores = batch->scores;
+  p.positions = batch->positions;
+  p.err = batch->error;
+  const long long warps = rows + static_cast<long long>(p.B) * (batch->page_size - 1);
+  if (warps > INT_MAX - 8) return KVC_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e =
+      launch_pdl(paged_append_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(paged_grow_kernel, dim3((p.B + 255) / 256), dim3(256), 0, s, row_start_dev, batch->lengths,
+                   batch->next_positions, p.B, rows, batch->max_pages * batch->page_size);
+  return status_of(e);
+}
+
+extern "C" kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
+                                       void* o_dev, float* lse_dev, int32_t rows, const int32_t* row_start_dev,
+                                       int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  using namespace kvc;
+  if (!valid_batch(batch) || !row_start_dev || !valid_rows(batch, q_dev, q_row_stride, batch->num_q_heads, rows) ||
+      !aligned16(o_dev) || (rows > 0 && !o_dev) || !workspace_dev || !aligned16(workspace_dev) ||
+      (causal != 0 && causal != 1) || static_cast<long long>(rows) * batch->num_q_heads > (1LL << 32))
+    return KVC_ERR_ARG;
+  if (rows == 0) return KVC_OK;
+  const int sms = sm_count();
+  if (sms < 1) return KVC_ERR_CUDA;
+  PagedParams p = base_params(batch, rows, row_start_dev, sms);
+  attend_schedule(&p, batch);
+  const Layout l = attend_layout(p);
+  if (workspace_bytes < static_cast<int64_t>(l.bytes)) return KVC_ERR_ARG;
+  uint8_t* w = static_cast<uint8_t*>(workspace_dev);
+  p.plan = reinterpret_cast<long long*>(w + l.plan);
+  p.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
+  p.part_o = reinterpret_cast<float*>(w + l.part_o);
+  p.q = q_dev;
+  p.q_stride = q_row_stride;
+  p.o = o_dev;
+  p.lse = lse_dev;
+  p.causal = causal;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_paged_attend_simt(s, p, batch->dtype);
+  if (e == cudaSuccess) e = batch->dtype == KVC_F32 ? launch_merge<float>(s, p) : launch_merge<__nv_bfloat16>(s, p);
+  return status_of(e);
+}
+
+extern "C" kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
+                                        const float* lse_dev, int32_t rows, const int32_t* row_start_dev,
+                                        int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  using namespace kvc;
+  if (!valid_batch(batch) || !batch->scores || !row_start_dev ||
+      !valid_rows(batch, q_dev, q_row_stride, batch->num_q_heads, rows) || (rows > 0 && !lse_dev) || !workspace_dev ||
+      !aligned16(workspace_dev) || (causal != 0 && causal != 1))
+    return KVC_ERR_ARG;
+  if (rows == 0) return KVC_OK;
+  const int sms = sm_count();
+  if (sms < 1) return KVC_ERR_CUDA;
+  PagedParams p = base_params(batch, rows, row_start_dev, sms);
+  weights_schedule(&p);
+  const Layout l = weights_layout(p);
+  if (workspace_bytes < static_cast<int64_t>(l.bytes)) return KVC_ERR_ARG;
+  uint8_t* w = static_cast<uint8_t*>(workspace_dev);
+  p.plan = reinterpret_cast<long long*>(w + l.plan);
+  p.part_id = reinterpret_cast<int4*>(w + l.part_id);
+  p.part_w = reinterpret_cast<float*>(w + l.part_w);
+  p.q = q_dev;
+  p.q_stride = q_row_stride;
+  p.lse = const_cast<float*>(lse_dev);
+  p.scores = batch->scores;
+  p.causal = causal;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_paged_weights_simt(s, p, batch->dtype);
+  // one tile of rows holds every sequence's: no key block is split
+  if (e == cudaSuccess && rows > p.tile_tokens)
+    e = launch_pdl(paged_weights_merge_kernel, dim3(p.grid), dim3(256), 0, s, p);
+  return status_of(e);
+}
+
+extern "C" kvc_status kvc_paged_evict(const kvc_paged_batch* batch, int32_t keep, int32_t sinks, int32_t recent,
+                                      void* workspace_dev, int64_t workspace_bytes, void* stream) {
+  using namespace kvc;
+  if (!valid_batch(batch) || !batch->scores || !batch->positions || !batch->next_positions || keep < 1 || sinks < 0 ||
+      recent < 0 || static_cast<long long>(sinks) + recent > keep || !workspace_dev || !aligned16(workspace_dev) ||
+      workspace_bytes < static_cast<int64_t>(evict_bytes(batch, keep)))
+    return KVC_ERR_ARG;
+  const long long cap = static_cast<long long>(batch->max_pages) * batch->page_size;
+  if (cap <= keep) return KVC_OK;              // no sequence can be longer
+  if (cap > paged_evict_max_slots()) return KVC_ERR_UNSUPPORTED;
+  EvictParams p{};
+  p.B = batch->num_seqs;
+  p.Hkv = batch->num_kv_heads;
+  p.page_shift = page_shift(batch->page_size);
+  p.max_pages = batch->max_pages;
+  p.row_bytes = batch->head_dim * (batch->dtype == KVC_F32 ? 4 : 2);
+  p.keep = keep;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.pool_pages = batch->pool_pages;
+  p.page_table = batch->page_table;
+  p.lengths = batch->lengths;
+  p.next_positions = batch->next_positions;
+  p.k_pool = static_cast<uint8_t*>(batch->k_pool);
+  p.v_pool = static_cast<uint8_t*>(batch->v_pool);
+  p.scores = batch->scores;
+  p.positions = batch->positions;
+  p.moves = static_cast<int32_t*>(workspace_dev);
+  p.move_cap = move_cap(batch, keep);
+  p.err = batch->error;
+  return status_of(launch_paged_evict(static_cast<cudaStream_t>(stream), p, batch->lengths));
+}

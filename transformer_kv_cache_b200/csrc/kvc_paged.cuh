@@ -1,0 +1,328 @@
+// kvc_paged.cuh -- what the paged-batch operators share: the batch as the kernels see it, the
+// schedule of the attention and weight kernels, and the layout of their workspace.
+//
+// Schedule. The work of a call is a sequence of units; CTA c of the grid takes the units
+// [c * U, (c + 1) * U) with U = ceil(units / CTAs), whatever the lengths on the device are, so
+// a long sequence is split over CTAs and short ones share one, and no host copy of a length is
+// needed (a captured graph follows the lengths of its replay). A unit of attention is one key
+// tile of one item; an item is one KV head with up to item_tokens query tokens of one
+// sequence (its G query heads each), or, for the shared prefix, of the whole batch: there the
+// queries of all sequences are packed, so the prefix is read once for the batch and not once
+// per sequence. The prefix is sequence -1 of the schedule. An item whose units fall into several
+// CTAs leaves several partial results; the CTA that has its first unit puts its partial into
+// the row's own slot, every other CTA into the CTA's slot (a CTA continues at most one item,
+// the one it begins with).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvc_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace kvc {
+
+struct PagedParams {
+  int B, Hq, Hkv, G, D;
+  int page_shift;               // page size = 1 << page_shift
+  int max_pages;                // pages of a sequence's page-table row
+  int prefix_tokens;
+  int rows;                     // rows of Q (the tensors' size; row_start tells which are in use)
+  int causal;
+  long long pool_pages;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* prefix_pages;
+  const int32_t* row_start;
+  const void* q;
+  long long q_stride;           // elements between Q rows
+  const void* k_pool;
+  const void* v_pool;
+  void* o;
+  float* lse;                   // attention: out (may be null); weights: in
+  float* scores;
+  float scale_log2;             // softmax scale * log2(e)
+  int* err;
+  // schedule
+  int item_tokens;              // query tokens of an item
+  int tile_tokens;              // query tokens of a tile (item_tokens, or half of it)
+  int key_tile;                 // keys of a unit
+  int streams;                  // tiles of an item: 1, or 2 (an item of one tile splits its keys in two streams)
+  int slot_rows;                // rows of a CTA's partial slot
+  int grid;                     // CTAs of the schedule
+  // workspace
+  long long* plan;              // [0] U, [1 + b] first unit of sequence b (b = -1 starts at 0)
+  float* part_o;                // attention: [row slots | CTA slots][D]
+  float2* part_ml;              // their running maximum (base-2 logit) and sum
+  float* part_w;                // weights: [CTA][slot_rows] sums of continued items
+  int4* part_id;                // weights: [CTA] (b, h, key block, 1 when it continues an item)
+};
+
+struct SeqView {
+  int r0, n, len;               // first row, rows, keys
+};
+
+__device__ __forceinline__ int paged_cap(const PagedParams& p) { return p.max_pages << p.page_shift; }
+
+// Sequence b (-1: the prefix and the whole batch's rows), clamped into the tensors.
+__device__ __forceinline__ SeqView seq_view(const PagedParams& p, int b) {
+  SeqView v;
+  const int lo = b < 0 ? p.row_start[0] : p.row_start[b];
+  const int hi = b < 0 ? p.row_start[p.B] : p.row_start[b + 1];
+  v.r0 = min(max(lo, 0), p.rows);
+  v.n = min(max(hi, v.r0), p.rows) - v.r0;
+  v.len = b < 0 ? p.prefix_tokens : min(max(p.lengths[b], 0), paged_cap(p));
+  return v;
+}
+// Latch an error when sequence b's length or rows are outside its tensors.
+__device__ __forceinline__ void seq_check(const PagedParams& p, int b) {
+  const int lo = p.row_start[b], hi = p.row_start[b + 1], len = p.lengths[b];
+  if (lo < 0 || hi < lo || hi > p.rows || len < 0 || len > paged_cap(p)) latch_error(p.err, DERR_BOUNDS);
+}
+
+__device__ __forceinline__ int seq_items(const PagedParams& p, const SeqView& v) {
+  return (v.n + p.item_tokens - 1) / p.item_tokens;
+}
+// Keys that some row among the first t tokens of the sequence sees.
+__device__ __forceinline__ int keys_before(const PagedParams& p, int b, const SeqView& v, int t) {
+  return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t)) : v.len;
+}
+__device__ __forceinline__ int item_units(const PagedParams& p, int b, const SeqView& v, int i) {
+  const int t = min(v.n, (i + 1) * p.item_tokens);
+  return (keys_before(p, b, v, t) + p.key_tile - 1) / p.key_tile;
+}
+// Units of a sequence's items [0, i) for one head.
+__device__ __forceinline__ long long units_before(const PagedParams& p, int b, const SeqView& v, int i) {
+  if (b < 0 || !p.causal) return static_cast<long long>(i) * item_units(p, b, v, 0);
+  long long s = 0;
+  for (int j = 0; j < i; ++j) s += item_units(p, b, v, j);
+  return s;
+}
+__device__ __forceinline__ long long head_units(const PagedParams& p, int b, const SeqView& v) {
+  return units_before(p, b, v, seq_items(p, v));
+}
+
+// The schedule's walk through a CTA's units.
+struct Segment {
+  int b, h, i;                  // sequence, KV head, item
+  SeqView v;
+  int k0, k1;                   // key tiles [k0, k1) of the item
+};
+struct Walk {
+  long long u, u1;              // units left
+  long long item_first;         // first unit of the item (b, h, i)
+  int b, h, i;
+  SeqView v;
+  int items;
+};
+
+// Block-wide: the first unit of every sequence, and this CTA's place in them. `first_of(b)`
+// gives the units of one head of sequence b. Every thread of the block calls it; s must hold
+// 2 + blockDim.x / 32 long longs. CTA 0 writes the plan.
+template <typename HeadUnits>
+__device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, HeadUnits&& units_of_head) {
+  const int nt = blockDim.x, t = threadIdx.x;
+  const int lane = t & 31, warp = t >> 5, warps = nt >> 5;
+  const int b_first = p.prefix_tokens > 0 ? -1 : 0;
+  const int n_seq = p.B - b_first;
+  const int per = (n_seq + nt - 1) / nt;
+  const int b0 = b_first + min(n_seq, t * per), b1 = b_first + min(n_seq, (t + 1) * per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (blockIdx.x == 0 && b >= 0) seq_check(p, b);
+    mine += p.Hkv * units_of_head(b, seq_view(p, b));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s[2 + warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    const long long x = s[2 + w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  before += incl - mine;
+  const long long U = (total + p.grid - 1) / p.grid;
+  const long long u0 = min(total, U * blockIdx.x), u1 = min(total, u0 + U);
+  if (blockIdx.x == 0) {
+    if (t == 0) p.plan[0] = U;
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      if (b >= 0) p.plan[1 + b] = at;
+      at += p.Hkv * units_of_head(b, seq_view(p, b));
+    }
+  }
+  // the thread whose sequences hold unit u0 finds the one
+  if (u0 < u1 && u0 >= before && u0 < before + mine) {
+    long long at = before;
+    int b = b0;
+    for (;; ++b) {
+      const long long x = p.Hkv * units_of_head(b, seq_view(p, b));
+      if (u0 < at + x) break;
+      at += x;
+    }
+    s[0] = at;
+    s[1] = b;
+  }
+  __syncthreads();
+  Walk w{};
+  w.u = u0;
+  w.u1 = u1;
+  if (u0 < u1) {
+    w.b = static_cast<int>(s[1]);
+    w.v = seq_view(p, w.b);
+    w.items = seq_items(p, w.v);
+    const long long uph = units_of_head(w.b, w.v);
+    w.h = static_cast<int>((u0 - s[0]) / uph);
+    w.item_first = s[0] + w.h * uph;
+    w.i = 0;
+  }
+  return w;
+}
+
+// The next piece of one item in the CTA's units (attention: units are key tiles of items).
+__device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segment& g) {
+  while (w.u < w.u1) {
+    if (w.i >= w.items) {
+      w.i = 0;
+      if (++w.h >= p.Hkv) {
+        w.h = 0;
+        ++w.b;
+        w.v = seq_view(p, w.b);
+        w.items = seq_items(p, w.v);
+      }
+      continue;
+    }
+    const int nk = item_units(p, w.b, w.v, w.i);
+    if (w.u >= w.item_first + nk) {
+      w.item_first += nk;
+      ++w.i;
+      continue;
+    }
+    g.b = w.b;
+    g.h = w.h;
+    g.i = w.i;
+    g.v = w.v;
+    g.k0 = static_cast<int>(w.u - w.item_first);
+    g.k1 = static_cast<int>(min(static_cast<long long>(nk), w.u1 - w.item_first));
+    w.u = w.item_first + g.k1;
+    return true;
+  }
+  return false;
+}
+
+// Physical page of key `slot` of sequence b; -1 (and an error) when the table names none.
+__device__ __forceinline__ long long page_of(const PagedParams& p, int b, int slot) {
+  const int k = slot >> p.page_shift;
+  const int32_t page = b < 0 ? __ldg(p.prefix_pages + k)
+                             : __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + k);
+  if (page < 0 || page >= p.pool_pages) {
+    latch_error(p.err, DERR_BOUNDS);
+    return -1;
+  }
+  return page;
+}
+// Row of the pool (rows of D elements) that holds key `slot` of sequence b for KV head h, or -1.
+__device__ __forceinline__ long long pool_row(const PagedParams& p, int b, int h, int slot) {
+  const long long page = page_of(p, b, slot);
+  return page < 0 ? -1 : (((page * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1)));
+}
+// Keys that token t of the sequence sees.
+__device__ __forceinline__ int key_limit(const PagedParams& p, int b, const SeqView& v, int t) {
+  return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t + 1)) : v.len;
+}
+
+// Partial slots. Row slots: [prefix or own][stream][row][query head]; CTA slots after them.
+__host__ __device__ __forceinline__ long long row_slots(long long rows, int Hq, int streams, bool prefix) {
+  return (prefix ? 2LL : 1LL) * streams * rows * Hq;
+}
+__device__ __forceinline__ long long row_slot(const PagedParams& p, int b, int stream, int row, int hq) {
+  const int part = p.prefix_tokens > 0 && b >= 0 ? 1 : 0;
+  return ((static_cast<long long>(part) * p.streams + stream) * p.rows + row) * p.Hq + hq;
+}
+__device__ __forceinline__ long long cta_slot(const PagedParams& p, int cta, int r) {
+  return row_slots(p.rows, p.Hq, p.streams, p.prefix_tokens > 0) + static_cast<long long>(cta) * p.slot_rows + r;
+}
+
+// Sequence whose rows hold `row` (row_start[b] <= row < row_start[b + 1]), or -1; warp-wide.
+__device__ __forceinline__ int find_sequence(const int32_t* row_start, int B, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B + 1;                                 // row_start entries [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < n && row_start[lo + at] <= row;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    if (m == 0) return -1;
+    const int k = 31 - __clz(m);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  if (lo >= B) return -1;
+  return row_start[lo] <= row && row < row_start[lo + 1] ? lo : -1;
+}
+
+// Weights: a unit is one key block (key_tile keys of a sequence, one KV head) with one tile of
+// query tokens, tiles running fastest, so that a key block's sums stay in a CTA.
+__device__ __forceinline__ long long weight_head_units(const PagedParams& p, const SeqView& v) {
+  return static_cast<long long>((v.len + p.key_tile - 1) / p.key_tile) *
+         ((v.n + p.tile_tokens - 1) / p.tile_tokens);
+}
+struct WeightSegment {
+  int b, h, kb;                 // sequence, KV head, key block
+  SeqView v;
+  int t0, t1;                   // query tiles [t0, t1)
+};
+__device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& w, WeightSegment& g) {
+  while (w.u < w.u1) {
+    const long long uph = weight_head_units(p, w.v);
+    if (w.u >= w.item_first + uph) {
+      w.item_first += uph;
+      if (++w.h >= p.Hkv) {
+        w.h = 0;
+        ++w.b;
+        w.v = seq_view(p, w.b);
+      }
+      continue;
+    }
+    const int tiles = (w.v.n + p.tile_tokens - 1) / p.tile_tokens;
+    const long long rel = w.u - w.item_first;
+    g.b = w.b;
+    g.h = w.h;
+    g.v = w.v;
+    g.kb = static_cast<int>(rel / tiles);
+    g.t0 = static_cast<int>(rel - static_cast<long long>(g.kb) * tiles);
+    g.t1 = static_cast<int>(min(static_cast<long long>(tiles), g.t0 + (w.u1 - w.u)));
+    w.u += g.t1 - g.t0;
+    return true;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------ launchers
+cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p, int dtype);
+cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype);
+struct EvictParams {
+  int B, Hkv, page_shift, max_pages, row_bytes;
+  int keep, sinks, recent;
+  long long pool_pages;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* next_positions;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* scores;
+  int32_t* positions;
+  int32_t* moves;               // workspace: [B * Hkv][2][move_cap] slots moved to and from
+  int move_cap;
+  int* err;
+};
+int paged_evict_max_slots();
+cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int32_t* lengths);
+
+}  // namespace kvc

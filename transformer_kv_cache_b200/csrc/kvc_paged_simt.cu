@@ -1,0 +1,283 @@
+// kvc_paged_simt.cu -- attention of a paged batch and the weights of its cached tokens in fp32
+// arithmetic (FFMA), with the schedule of kvc_paged.cuh.
+//
+// Attention: one pass over an item's keys with the running maximum and sum of the softmax; 256
+// threads as 16 x 16, a thread holding ROWS / 16 query rows by 4 keys of the scores and
+// ROWS / 16 rows by D / 16 columns of the output in registers. Weights: the same products with
+// keys and rows exchanged, so that a key's sum over the query rows stays in one half-warp.
+#include <math_constants.h>
+
+#include "kvc_paged.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kKT = 64;                        // keys of a tile
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// Keys [key0, key0 + kKT) of one pool into shared memory as fp32; keys from `end` on are zeros.
+template <typename T, int D, int LD>
+__device__ __forceinline__ void load_keys(const PagedParams& p, const void* pool, int b, int h, int key0, int end,
+                                          float* dst) {
+  constexpr int kChunks = D / 4;
+  for (int i = threadIdx.x; i < kKT * kChunks; i += kThreads) {
+    const int key = i / kChunks, c = i % kChunks;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key0 + key < end) {
+      const long long row = pool_row(p, b, h, key0 + key);
+      if (row >= 0) x = load4(static_cast<const T*>(pool) + row * D + c * 4);
+    }
+    *reinterpret_cast<float4*>(dst + key * LD + c * 4) = x;
+  }
+}
+// The tile's query rows [token t0 .., G heads each] as fp32; rows past `tokens` are zeros.
+template <typename T, int D, int LD, int ROWS>
+__device__ __forceinline__ void load_queries(const PagedParams& p, const SeqView& v, int h, int t0, int rows,
+                                             float* dst) {
+  constexpr int kChunks = D / 4;
+  for (int i = threadIdx.x; i < ROWS * kChunks; i += kThreads) {
+    const int r = i / kChunks, c = i % kChunks;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      const long long row = v.r0 + t0 + r / p.G;
+      x = load4(static_cast<const T*>(p.q) + row * p.q_stride + (h * p.G + r % p.G) * D + c * 4);
+    }
+    *reinterpret_cast<float4*>(dst + r * LD + c * 4) = x;
+  }
+}
+
+// Scores of RA rows of `a` by RB rows of `b`, rows ra + i * sa and rb + j * sb.
+template <int D, int RA, int RB>
+__device__ __forceinline__ void dots(const float* a, int lda, int sa, const float* b, int ldb, int sb,
+                                     float (&s)[RA][RB]) {
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int j = 0; j < RB; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 x[RA], y[RB];
+#pragma unroll
+    for (int i = 0; i < RA; ++i) x[i] = load4(a + i * sa * lda + d);
+#pragma unroll
+    for (int j = 0; j < RB; ++j) y[j] = load4(b + j * sb * ldb + d);
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+        s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
+  }
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const PagedParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int LD = D + 4, RPT = ROWS / 16, LP = kKT + 4;
+  extern __shared__ float sm[];
+  float* qs = sm;                              // [ROWS][LD]
+  float* ks = qs + ROWS * LD;                  // [kKT][LD]
+  float* vs = ks + kKT * LD;                   // [kKT][LD]
+  float* ps = vs + kKT * LD;                   // [ROWS][LP]
+  __shared__ long long plan_s[2 + kThreads / 32];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  Walk w = plan_walk(p, plan_s, [&](int b, const SeqView& v) { return head_units(p, b, v); });
+  Segment g;
+  while (next_segment(p, w, g)) {
+    const int t0 = g.i * p.item_tokens;
+    const int tokens = min(p.item_tokens, g.v.n - t0), rows = tokens * p.G;
+    __syncthreads();
+    load_queries<T, D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
+    float m[RPT], l[RPT], acc[RPT][D / 16];
+    int limit[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      m[r] = -CUDART_INF_F;
+      l[r] = 0.f;
+      const int at = ty * RPT + r;
+      limit[r] = at < rows ? key_limit(p, g.b, g.v, t0 + at / p.G) : 0;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
+    }
+    for (int kt = g.k0; kt < g.k1; ++kt) {
+      const int key0 = kt * kKT;
+      __syncthreads();
+      load_keys<T, D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
+      load_keys<T, D, LD>(p, p.v_pool, g.b, g.h, key0, g.v.len, vs);
+      __syncthreads();
+      float s[RPT][4];
+      dots<D, RPT, 4>(qs + ty * RPT * LD, LD, 1, ks + tx * LD, LD, 16, s);
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) {
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[r][j] = key0 + tx + 16 * j < limit[r] ? s[r][j] * p.scale_log2 : -CUDART_INF_F;
+          mx = fmaxf(mx, s[r][j]);
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float m_new = fmaxf(m[r], mx);
+        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // nothing visible yet: every weight is 0
+        const float f = exp2f(m[r] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(s[r][j] - base);
+          sum += e;
+          ps[(ty * RPT + r) * LP + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[r] = l[r] * f + sum;
+        m[r] = m_new;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[r][c] *= f;
+      }
+      __syncwarp();                            // a row's weights are written and read by one half-warp
+      for (int k = 0; k < kKT; k += 4) {
+        float4 pr[RPT];
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) pr[r] = load4(ps + (ty * RPT + r) * LP + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const float4 v4 = load4(vs + (k + kk) * LD + c * 64 + tx * 4);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+              const float e = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
+              acc[r][4 * c + 0] = fmaf(e, v4.x, acc[r][4 * c + 0]);
+              acc[r][4 * c + 1] = fmaf(e, v4.y, acc[r][4 * c + 1]);
+              acc[r][4 * c + 2] = fmaf(e, v4.z, acc[r][4 * c + 2]);
+              acc[r][4 * c + 3] = fmaf(e, v4.w, acc[r][4 * c + 3]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const int at = ty * RPT + r;
+      if (at >= rows) continue;
+      const long long slot = g.k0 == 0 ? row_slot(p, g.b, 0, g.v.r0 + t0 + at / p.G, g.h * p.G + at % p.G)
+                                       : cta_slot(p, blockIdx.x, at);
+      if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        *reinterpret_cast<float4*>(p.part_o + slot * D + c * 64 + tx * 4) =
+            make_float4(acc[r][4 * c], acc[r][4 * c + 1], acc[r][4 * c + 2], acc[r][4 * c + 3]);
+    }
+  }
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const PagedParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int LD = D + 4, RPT = ROWS / 16;
+  extern __shared__ float sm[];
+  float* qs = sm;                              // [ROWS][LD]
+  float* ks = qs + ROWS * LD;                  // [kKT][LD]
+  __shared__ long long plan_s[2 + kThreads / 32];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  Walk w = plan_walk(p, plan_s, [&](int, const SeqView& v) { return weight_head_units(p, v); });
+  if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
+  WeightSegment g;
+  while (next_weight_segment(p, w, g)) {
+    const int key0 = g.kb * kKT;
+    __syncthreads();
+    load_keys<T, D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = g.t0; t < g.t1; ++t) {
+      const int tok0 = t * p.tile_tokens;
+      const int rows = min(p.tile_tokens, g.v.n - tok0) * p.G;
+      __syncthreads();
+      load_queries<T, D, LD, ROWS>(p, g.v, g.h, tok0, rows, qs);
+      __syncthreads();
+      float s[4][RPT];
+      dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
+        const int r = tx + 16 * j;
+        if (r < rows) {
+          const int tok = tok0 + r / p.G;
+          const int limit = key_limit(p, g.b, g.v, tok);
+          const float lse2 =
+              p.lse[static_cast<long long>(g.v.r0 + tok) * p.Hq + g.h * p.G + r % p.G] * 1.4426950408889634f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key0 + ty * 4 + i < limit) sum[i] += exp2f(fmaf(s[i][j], p.scale_log2, -lse2));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 8; d; d >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+    if (tx == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = key0 + ty * 4 + i;
+        if (g.t0 > 0)
+          p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + ty * 4 + i] = sum[i];
+        else if (key < g.v.len)
+          p.scores[(static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key] += sum[i];
+      }
+    }
+    if (g.t0 > 0 && threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.kb, 1);
+  }
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t attend(cudaStream_t s, const PagedParams& p) {
+  constexpr size_t smem = sizeof(float) * (ROWS * (D + 4) + 2 * kKT * (D + 4) + ROWS * (kKT + 4));
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<T, D, ROWS>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  });
+  return e != cudaSuccess ? e : launch_pdl(paged_attend_simt_kernel<T, D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
+}
+template <typename T, int D, int ROWS>
+cudaError_t weights(cudaStream_t s, const PagedParams& p) {
+  constexpr size_t smem = sizeof(float) * (ROWS + kKT) * (D + 4);
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_simt_kernel<T, D, ROWS>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  });
+  return e != cudaSuccess ? e
+                          : launch_pdl(paged_weights_simt_kernel<T, D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p, int dtype) {
+  const bool few = p.tile_tokens * p.G <= 16;
+  if (dtype == KVC_F32) {
+    if (p.D == 64) return few ? attend<float, 64, 16>(s, p) : attend<float, 64, 64>(s, p);
+    return few ? attend<float, 128, 16>(s, p) : attend<float, 128, 64>(s, p);
+  }
+  if (p.D == 64) return few ? attend<__nv_bfloat16, 64, 16>(s, p) : attend<__nv_bfloat16, 64, 64>(s, p);
+  return few ? attend<__nv_bfloat16, 128, 16>(s, p) : attend<__nv_bfloat16, 128, 64>(s, p);
+}
+
+cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype) {
+  const bool few = p.tile_tokens * p.G <= 16;
+  if (dtype == KVC_F32) {
+    if (p.D == 64) return few ? weights<float, 64, 16>(s, p) : weights<float, 64, 64>(s, p);
+    return few ? weights<float, 128, 16>(s, p) : weights<float, 128, 64>(s, p);
+  }
+  if (p.D == 64) return few ? weights<__nv_bfloat16, 64, 16>(s, p) : weights<__nv_bfloat16, 64, 64>(s, p);
+  return few ? weights<__nv_bfloat16, 128, 16>(s, p) : weights<__nv_bfloat16, 128, 64>(s, p);
+}
+
+}  // namespace kvc
