@@ -1,5 +1,7 @@
 // kvc_paged.cu -- the paged-batch entry points (kvc_paged_*): argument checks, workspace,
 // the append and the merge of partial attention results.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -84,6 +86,15 @@ PagedParams base_params(const kvc_paged_batch* b, int32_t rows, const int32_t* r
 
 void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->prefix_tokens = b->prefix_tokens;
+  if (b->dtype == KVC_BF16) {
+    // two tiles of 128 packed rows share a CTA's key tiles
+    p->tile_tokens = 128 / p->G;
+    p->item_tokens = 2 * p->tile_tokens;
+    p->key_tile = 128;
+    p->streams = 2;
+    p->slot_rows = 256;
+    return;
+  }
   // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend
   // its products on padding), else of 64
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
@@ -130,6 +141,18 @@ int move_cap(const kvc_paged_batch* b, int32_t keep) {
 }
 size_t evict_bytes(const kvc_paged_batch* b, int32_t keep) {
   return align256(sizeof(int32_t) * 2 * static_cast<size_t>(b->num_seqs) * b->num_kv_heads * move_cap(b, keep));
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
+               : nullptr;
+  }();
+  return fn;
 }
 
 // ------------------------------------------------------------------ append
@@ -317,6 +340,33 @@ __global__ void __launch_bounds__(256) paged_weights_merge_kernel(const PagedPar
 kvc_status status_of(cudaError_t e) { return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA; }
 
 }  // namespace
+
+bool encode_rows_tmap(CUtensorMap* map, const void* rows_dev, const PagedParams& p) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.Hq),
+                              static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.D) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.tile_tokens)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows_dev), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_slots_tmap(CUtensorMap* map, const void* pool, const PagedParams& p) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.D),
+                              static_cast<cuuint64_t>((p.pool_pages * p.Hkv) << p.page_shift)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.D) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(std::min(1 << p.page_shift, 128))};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kvc
 
 extern "C" kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t rows, int32_t keep,
@@ -404,7 +454,7 @@ extern "C" kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void*
   p.lse = lse_dev;
   p.causal = causal;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_paged_attend_simt(s, p, batch->dtype);
+  cudaError_t e = batch->dtype == KVC_BF16 ? launch_paged_attend_tc(s, p) : launch_paged_attend_simt(s, p);
   if (e == cudaSuccess) e = batch->dtype == KVC_F32 ? launch_merge<float>(s, p) : launch_merge<__nv_bfloat16>(s, p);
   return status_of(e);
 }

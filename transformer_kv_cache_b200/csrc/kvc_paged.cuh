@@ -305,7 +305,14 @@ __device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& 
 }
 
 // ------------------------------------------------------------------ launchers
-cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p, int dtype);
+// Tensor maps of the bf16 kernels. Query rows as (dims, heads, rows), one box a 64-dim half of
+// the G heads of tile_tokens rows; pool slots as (dims, pool rows), one box a 64-dim half of a
+// page's slots (128 of them at most).
+bool encode_rows_tmap(CUtensorMap* map, const void* rows_dev, const PagedParams& p);
+bool encode_slots_tmap(CUtensorMap* map, const void* pool, const PagedParams& p);
+
+cudaError_t launch_paged_attend_tc(cudaStream_t s, const PagedParams& p);
+cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p);
 cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype);
 struct EvictParams {
   int B, Hkv, page_shift, max_pages, row_bytes;

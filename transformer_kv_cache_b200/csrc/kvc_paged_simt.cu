@@ -260,14 +260,10 @@ cudaError_t weights(cudaStream_t s, const PagedParams& p) {
 
 }  // namespace
 
-cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p, int dtype) {
-  const bool few = p.tile_tokens * p.G <= 16;
-  if (dtype == KVC_F32) {
-    if (p.D == 64) return few ? attend<float, 64, 16>(s, p) : attend<float, 64, 64>(s, p);
-    return few ? attend<float, 128, 16>(s, p) : attend<float, 128, 64>(s, p);
-  }
-  if (p.D == 64) return few ? attend<__nv_bfloat16, 64, 16>(s, p) : attend<__nv_bfloat16, 64, 64>(s, p);
-  return few ? attend<__nv_bfloat16, 128, 16>(s, p) : attend<__nv_bfloat16, 128, 64>(s, p);
+cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p) {
+  const bool few = p.slot_rows == 16;
+  if (p.D == 64) return few ? attend<float, 64, 16>(s, p) : attend<float, 64, 64>(s, p);
+  return few ? attend<float, 128, 16>(s, p) : attend<float, 128, 64>(s, p);
 }
 
 cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype) {
