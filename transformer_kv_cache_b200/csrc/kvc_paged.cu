@@ -105,8 +105,14 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->grid *= 2;
 }
 
-void weights_schedule(PagedParams* p) {
+void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->prefix_tokens = 0;                        // the prefix keeps no scores
+  if (b->dtype == KVC_BF16) {
+    p->tile_tokens = p->item_tokens = 128 / p->G;
+    p->key_tile = p->slot_rows = 256;
+    p->streams = 1;
+    return;
+  }
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
   p->tile_tokens = p->item_tokens = (per_seq <= 16 ? 16 : 64) / p->G;
   p->key_tile = 64;
@@ -380,7 +386,7 @@ extern "C" kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t 
   attend_schedule(&p, batch);
   most = std::max(most, attend_layout(p).bytes);
   p = base_params(batch, rows, nullptr, sms);
-  weights_schedule(&p);
+  weights_schedule(&p, batch);
   most = std::max(most, weights_layout(p).bytes);
   most = std::max(most, evict_bytes(batch, keep));
   *bytes_out = static_cast<int64_t>(most);
@@ -471,7 +477,7 @@ extern "C" kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void
   const int sms = sm_count();
   if (sms < 1) return KVC_ERR_CUDA;
   PagedParams p = base_params(batch, rows, row_start_dev, sms);
-  weights_schedule(&p);
+  weights_schedule(&p, batch);
   const Layout l = weights_layout(p);
   if (workspace_bytes < static_cast<int64_t>(l.bytes)) return KVC_ERR_ARG;
   uint8_t* w = static_cast<uint8_t*>(workspace_dev);
@@ -484,7 +490,7 @@ extern "C" kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void
   p.scores = batch->scores;
   p.causal = causal;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_paged_weights_simt(s, p, batch->dtype);
+  cudaError_t e = batch->dtype == KVC_BF16 ? launch_paged_weights_tc(s, p) : launch_paged_weights_simt(s, p);
   // one tile of rows holds every sequence's: no key block is split
   if (e == cudaSuccess && rows > p.tile_tokens)
     e = launch_pdl(paged_weights_merge_kernel, dim3(p.grid), dim3(256), 0, s, p);

@@ -313,7 +313,8 @@ bool encode_slots_tmap(CUtensorMap* map, const void* pool, const PagedParams& p)
 
 cudaError_t launch_paged_attend_tc(cudaStream_t s, const PagedParams& p);
 cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p);
-cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype);
+cudaError_t launch_paged_weights_tc(cudaStream_t s, const PagedParams& p);
+cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p);
 struct EvictParams {
   int B, Hkv, page_shift, max_pages, row_bytes;
   int keep, sinks, recent;

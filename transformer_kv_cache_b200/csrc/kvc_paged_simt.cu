@@ -1,5 +1,5 @@
 // kvc_paged_simt.cu -- attention of a paged batch and the weights of its cached tokens in fp32
-// arithmetic (FFMA), with the schedule of kvc_paged.cuh.
+// storage and arithmetic (FFMA), with the schedule of kvc_paged.cuh.
 //
 // Attention: one pass over an item's keys with the running maximum and sum of the softmax; 256
 // threads as 16 x 16, a thread holding ROWS / 16 query rows by 4 keys of the scores and
@@ -16,14 +16,9 @@ constexpr int kKT = 64;                        // keys of a tile
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
 
-// Keys [key0, key0 + kKT) of one pool into shared memory as fp32; keys from `end` on are zeros.
-template <typename T, int D, int LD>
+// Keys [key0, key0 + kKT) of one pool into shared memory; keys from `end` on are zeros.
+template <int D, int LD>
 __device__ __forceinline__ void load_keys(const PagedParams& p, const void* pool, int b, int h, int key0, int end,
                                           float* dst) {
   constexpr int kChunks = D / 4;
@@ -32,13 +27,13 @@ __device__ __forceinline__ void load_keys(const PagedParams& p, const void* pool
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (key0 + key < end) {
       const long long row = pool_row(p, b, h, key0 + key);
-      if (row >= 0) x = load4(static_cast<const T*>(pool) + row * D + c * 4);
+      if (row >= 0) x = load4(static_cast<const float*>(pool) + row * D + c * 4);
     }
     *reinterpret_cast<float4*>(dst + key * LD + c * 4) = x;
   }
 }
-// The tile's query rows [token t0 .., G heads each] as fp32; rows past `tokens` are zeros.
-template <typename T, int D, int LD, int ROWS>
+// The tile's query rows [token t0 .., G heads each]; rows past `tokens` are zeros.
+template <int D, int LD, int ROWS>
 __device__ __forceinline__ void load_queries(const PagedParams& p, const SeqView& v, int h, int t0, int rows,
                                              float* dst) {
   constexpr int kChunks = D / 4;
@@ -47,7 +42,7 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, const SeqView
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows) {
       const long long row = v.r0 + t0 + r / p.G;
-      x = load4(static_cast<const T*>(p.q) + row * p.q_stride + (h * p.G + r % p.G) * D + c * 4);
+      x = load4(static_cast<const float*>(p.q) + row * p.q_stride + (h * p.G + r % p.G) * D + c * 4);
     }
     *reinterpret_cast<float4*>(dst + r * LD + c * 4) = x;
   }
@@ -76,7 +71,7 @@ __device__ __forceinline__ void dots(const float* a, int lda, int sa, const floa
   }
 }
 
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const PagedParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -94,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
     const int t0 = g.i * p.item_tokens;
     const int tokens = min(p.item_tokens, g.v.n - t0), rows = tokens * p.G;
     __syncthreads();
-    load_queries<T, D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
+    load_queries<D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
     float m[RPT], l[RPT], acc[RPT][D / 16];
     int limit[RPT];
 #pragma unroll
@@ -109,8 +104,8 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
     for (int kt = g.k0; kt < g.k1; ++kt) {
       const int key0 = kt * kKT;
       __syncthreads();
-      load_keys<T, D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
-      load_keys<T, D, LD>(p, p.v_pool, g.b, g.h, key0, g.v.len, vs);
+      load_keys<D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
+      load_keys<D, LD>(p, p.v_pool, g.b, g.h, key0, g.v.len, vs);
       __syncthreads();
       float s[RPT][4];
       dots<D, RPT, 4>(qs + ty * RPT * LD, LD, 1, ks + tx * LD, LD, 16, s);
@@ -178,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
   }
 }
 
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const PagedParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -194,13 +189,13 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   while (next_weight_segment(p, w, g)) {
     const int key0 = g.kb * kKT;
     __syncthreads();
-    load_keys<T, D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
+    load_keys<D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = g.t0; t < g.t1; ++t) {
       const int tok0 = t * p.tile_tokens;
       const int rows = min(p.tile_tokens, g.v.n - tok0) * p.G;
       __syncthreads();
-      load_queries<T, D, LD, ROWS>(p, g.v, g.h, tok0, rows, qs);
+      load_queries<D, LD, ROWS>(p, g.v, g.h, tok0, rows, qs);
       __syncthreads();
       float s[4][RPT];
       dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
@@ -236,44 +231,40 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   }
 }
 
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 cudaError_t attend(cudaStream_t s, const PagedParams& p) {
   constexpr size_t smem = sizeof(float) * (ROWS * (D + 4) + 2 * kKT * (D + 4) + ROWS * (kKT + 4));
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<T, D, ROWS>),
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<D, ROWS>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
-  return e != cudaSuccess ? e : launch_pdl(paged_attend_simt_kernel<T, D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
+  return e != cudaSuccess ? e : launch_pdl(paged_attend_simt_kernel<D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
 }
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 cudaError_t weights(cudaStream_t s, const PagedParams& p) {
   constexpr size_t smem = sizeof(float) * (ROWS + kKT) * (D + 4);
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_simt_kernel<T, D, ROWS>),
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_simt_kernel<D, ROWS>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
   return e != cudaSuccess ? e
-                          : launch_pdl(paged_weights_simt_kernel<T, D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
+                          : launch_pdl(paged_weights_simt_kernel<D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p) {
   const bool few = p.slot_rows == 16;
-  if (p.D == 64) return few ? attend<float, 64, 16>(s, p) : attend<float, 64, 64>(s, p);
-  return few ? attend<float, 128, 16>(s, p) : attend<float, 128, 64>(s, p);
+  if (p.D == 64) return few ? attend<64, 16>(s, p) : attend<64, 64>(s, p);
+  return few ? attend<128, 16>(s, p) : attend<128, 64>(s, p);
 }
 
-cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p, int dtype) {
+cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p) {
   const bool few = p.tile_tokens * p.G <= 16;
-  if (dtype == KVC_F32) {
-    if (p.D == 64) return few ? weights<float, 64, 16>(s, p) : weights<float, 64, 64>(s, p);
-    return few ? weights<float, 128, 16>(s, p) : weights<float, 128, 64>(s, p);
-  }
-  if (p.D == 64) return few ? weights<__nv_bfloat16, 64, 16>(s, p) : weights<__nv_bfloat16, 64, 64>(s, p);
-  return few ? weights<__nv_bfloat16, 128, 16>(s, p) : weights<__nv_bfloat16, 128, 64>(s, p);
+  if (p.D == 64) return few ? weights<64, 16>(s, p) : weights<64, 64>(s, p);
+  return few ? weights<128, 16>(s, p) : weights<128, 64>(s, p);
 }
 
 }  // namespace kvc
