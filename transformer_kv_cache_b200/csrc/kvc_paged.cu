@@ -86,6 +86,10 @@ PagedParams base_params(const kvc_paged_batch* b, int32_t rows, const int32_t* r
 
 void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->prefix_tokens = b->prefix_tokens;
+  p->prefix_units = (b->prefix_tokens + (b->dtype == KVC_BF16 ? 128 : 64) - 1) / (b->dtype == KVC_BF16 ? 128 : 64);
+  // Where the sequences' rows fill their items (on average), packing the batch's rows saves no
+  // pass over the prefix: each item then reads the prefix before its own keys, and its rows'
+  // partials need no joining with those of a second item.
   if (b->dtype == KVC_BF16) {
     // two tiles of 128 packed rows share a CTA's key tiles
     p->tile_tokens = 128 / p->G;
@@ -93,6 +97,7 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
     p->key_tile = 128;
     p->streams = 2;
     p->slot_rows = 256;
+    p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens;
     return;
   }
   // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend
@@ -102,6 +107,7 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->tile_tokens = p->item_tokens = p->slot_rows / p->G;
   p->key_tile = 64;
   p->streams = 1;
+  p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens;
   p->grid *= 2;
 }
 
@@ -123,7 +129,7 @@ void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
 
 Layout attend_layout(const PagedParams& p) {
   Layout l{};
-  const size_t slots = static_cast<size_t>(row_slots(p.rows, p.Hq, p.streams, p.prefix_tokens > 0)) +
+  const size_t slots = static_cast<size_t>(row_slots(p)) +
                        static_cast<size_t>(p.grid) * p.slot_rows;
   l.plan = 0;
   l.part_ml = align256(8 * (static_cast<size_t>(p.B) + 1));
@@ -255,56 +261,109 @@ __global__ void paged_grow_kernel(const int32_t* row_start, int32_t* lengths, in
 // ------------------------------------------------------------------ merging partial results
 // One warp per (row, query head): O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the row's
 // partials in the order of their keys, LSE = ln 2 (M + log2 of that sum). A row that sees no key
-// gets O = 0 and LSE = -inf.
+// gets O = 0 and LSE = -inf. Rows that their CTA wrote itself are left alone. What the row needs
+// of the batch is read before the wait for the attention kernel (which had waited for whatever
+// wrote it), the partials after it.
+template <int D>
+struct Partial {
+  float m, l, o[D / 32];
+};
+template <int D>
+__device__ __forceinline__ Partial<D> load_partial(const PagedParams& p, long long slot, int lane) {
+  Partial<D> x;
+  const float2 ml = __ldcg(p.part_ml + slot);
+  x.m = ml.x;
+  x.l = ml.y;
+  if constexpr (D == 64) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + slot * D) + lane);
+    x.o[0] = v.x;
+    x.o[1] = v.y;
+  } else {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * D) + lane);
+    x.o[0] = v.x;
+    x.o[1] = v.y;
+    x.o[2] = v.z;
+    x.o[3] = v.w;
+  }
+  return x;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   constexpr int kPer = D / 32;
   const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int row = static_cast<int>(warp / p.Hq), hq = static_cast<int>(warp % p.Hq);
-  if (row >= p.rows) return;
-  const int b = find_sequence(p.row_start, p.B, row);
-  if (b < 0) return;                                   // behind the last sequence: left as it was
-  const long long U = p.plan[0];
+  const int b = row < p.rows ? find_sequence(p.row_start, p.B, row) : -1;
   const int h = hq / p.G, g = hq % p.G;
+  const int parts = parts_of(p);
+  // per part: units of the item, its first unit (without the sequence's), and the row's place
+  int nk[2] = {0, 0}, at[2], tile[2];
+  long long first[2];
+  bool split[2], whole = false;
+  if (b >= 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= parts) break;
+      const int s = parts == 2 && k == 0 ? -1 : b;
+      const SeqView v = seq_view(p, s);
+      const int t = row - v.r0;
+      const int item = t / p.item_tokens, in = t - item * p.item_tokens;
+      if (t < 0 || t >= v.n) continue;
+      nk[k] = item_units(p, s, v, item);
+      first[k] = h * head_units(p, s, v) + units_before(p, s, v, item);
+      split[k] = p.streams == 2 && v.n - item * p.item_tokens <= p.tile_tokens;
+      tile[k] = in / p.tile_tokens;
+      at[k] = (in - tile[k] * p.tile_tokens) * p.G + g;
+      whole = writes_rows(p, v, item);
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (b < 0) return;                                   // behind the last sequence: left as it was
+  const long long U = __ldcg(p.plan), own = __ldcg(p.plan + 1 + b);
   float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  auto add = [&](long long slot) {
-    const float2 ml = p.part_ml[slot];
-    if (ml.y == 0.f) return;                           // saw none of its keys
-    const float m = fmaxf(M, ml.x);
-    const float f0 = exp2f(M - m), f1 = exp2f(ml.x - m);
+  auto add = [&](const Partial<D>& x) {
+    if (x.l == 0.f) return;                            // saw none of its keys
+    const float m = fmaxf(M, x.m);
+    const float f0 = exp2f(M - m), f1 = exp2f(x.m - m);
     M = m;
-    L = L * f0 + ml.y * f1;
-    const float* src = p.part_o + slot * D + lane * kPer;
+    L = L * f0 + x.l * f1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f0 + src[i] * f1;
+    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f0 + x.o[i] * f1;
   };
-  for (int part = p.prefix_tokens > 0 ? 0 : 1; part < 2; ++part) {
-    const int s = part == 0 ? -1 : b;                  // the prefix's keys, then the sequence's own
-    const SeqView v = seq_view(p, s);
-    const int t = row - v.r0;
-    const int item = t / p.item_tokens, in = t - item * p.item_tokens;
-    const int nk = item_units(p, s, v, item);
-    if (nk > 0 && t >= 0 && t < v.n) {
-      const long long first = (s < 0 ? 0 : p.plan[1 + s]) + h * head_units(p, s, v) + units_before(p, s, v, item);
-      const bool split = p.streams == 2 && min(p.item_tokens, v.n - item * p.item_tokens) <= p.tile_tokens;
-      const int tile = in / p.tile_tokens;
-      const int r = (in - tile * p.tile_tokens) * p.G + g;
-      const int c0 = static_cast<int>(first / U), c1 = static_cast<int>((first + nk - 1) / U);
-      for (int c = c0; c <= c1; ++c)
-        for (int k = 0; k < (split ? 2 : 1); ++k)
-          add(c == c0 ? row_slot(p, s, k, row, hq)
-                      : cta_slot(p, c, (split ? k : tile) * (p.slot_rows / p.streams) + r));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k >= parts || nk[k] == 0) continue;
+    const int s = parts == 2 && k == 0 ? -1 : b;
+    const long long u0 = first[k] + (s < 0 ? 0 : own);
+    const int c0 = static_cast<int>(u0 / U), c1 = static_cast<int>((u0 + nk[k] - 1) / U);
+    if (c0 == c1 && whole) return;                     // written by its CTA
+    for (int c = c0; c <= c1; ++c) {
+      const long long s0 = c == c0 ? row_slot(p, s, 0, row, hq)
+                                   : cta_slot(p, c, (split[k] ? 0 : tile[k]) * (p.slot_rows / p.streams) + at[k]);
+      if (split[k]) {
+        const long long s1 = c == c0 ? row_slot(p, s, 1, row, hq) : cta_slot(p, c, p.slot_rows / p.streams + at[k]);
+        const Partial<D> x = load_partial<D>(p, s0, lane), y = load_partial<D>(p, s1, lane);
+        add(x);
+        add(y);
+      } else {
+        add(load_partial<D>(p, s0, lane));
+      }
     }
   }
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   T* out = static_cast<T*>(p.o) + (static_cast<long long>(row) * p.Hq + hq) * D + lane * kPer;
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) out[i] = static_cast<T>(acc[i] * inv);
+    for (int i = 0; i < kPer; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<float2*>(out + i) = make_float2(acc[i] * inv, acc[i + 1] * inv);
+  }
   if (p.lse && lane == 0)
     p.lse[static_cast<long long>(row) * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
@@ -363,12 +422,13 @@ bool encode_rows_tmap(CUtensorMap* map, const void* rows_dev, const PagedParams&
 bool encode_slots_tmap(CUtensorMap* map, const void* pool, const PagedParams& p) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.D),
-                              static_cast<cuuint64_t>((p.pool_pages * p.Hkv) << p.page_shift)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.D) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(std::min(1 << p.page_shift, 128))};
-  const cuuint32_t es[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box, es,
+  const cuuint64_t row = static_cast<cuuint64_t>(p.D) * 2;
+  const cuuint32_t halves = static_cast<cuuint32_t>(p.D / 64);
+  const cuuint64_t dims[4] = {64, 8, halves, static_cast<cuuint64_t>((p.pool_pages * p.Hkv) << p.page_shift) / 8};
+  const cuuint64_t strides[3] = {row, 128, row * 8};
+  const cuuint32_t box[4] = {64, 8, halves, static_cast<cuuint32_t>(std::min(1 << p.page_shift, 128)) / 8};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -384,6 +444,7 @@ extern "C" kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t 
   size_t most = 256;
   PagedParams p = base_params(batch, rows, nullptr, sms);
   attend_schedule(&p, batch);
+  p.join = 0;                                  // fewer rows may not join: this layout holds either
   most = std::max(most, attend_layout(p).bytes);
   p = base_params(batch, rows, nullptr, sms);
   weights_schedule(&p, batch);

@@ -29,6 +29,7 @@ struct PagedParams {
   int prefix_tokens;
   int rows;                     // rows of Q (the tensors' size; row_start tells which are in use)
   int causal;
+  int join;                     // 1: an item reads the prefix's key tiles before its own
   long long pool_pages;
   const int32_t* page_table;
   const int32_t* lengths;
@@ -47,6 +48,7 @@ struct PagedParams {
   int item_tokens;              // query tokens of an item
   int tile_tokens;              // query tokens of a tile (item_tokens, or half of it)
   int key_tile;                 // keys of a unit
+  int prefix_units;             // key tiles of the prefix
   int streams;                  // tiles of an item: 1, or 2 (an item of one tile splits its keys in two streams)
   int slot_rows;                // rows of a CTA's partial slot
   int grid;                     // CTAs of the schedule
@@ -67,11 +69,11 @@ __device__ __forceinline__ int paged_cap(const PagedParams& p) { return p.max_pa
 // Sequence b (-1: the prefix and the whole batch's rows), clamped into the tensors.
 __device__ __forceinline__ SeqView seq_view(const PagedParams& p, int b) {
   SeqView v;
-  const int lo = b < 0 ? p.row_start[0] : p.row_start[b];
-  const int hi = b < 0 ? p.row_start[p.B] : p.row_start[b + 1];
+  const int lo = __ldcg(p.row_start + (b < 0 ? 0 : b));
+  const int hi = __ldcg(p.row_start + (b < 0 ? p.B : b + 1));
   v.r0 = min(max(lo, 0), p.rows);
   v.n = min(max(hi, v.r0), p.rows) - v.r0;
-  v.len = b < 0 ? p.prefix_tokens : min(max(p.lengths[b], 0), paged_cap(p));
+  v.len = b < 0 ? p.prefix_tokens : min(max(__ldcg(p.lengths + b), 0), paged_cap(p));
   return v;
 }
 // Latch an error when sequence b's length or rows are outside its tensors.
@@ -83,19 +85,47 @@ __device__ __forceinline__ void seq_check(const PagedParams& p, int b) {
 __device__ __forceinline__ int seq_items(const PagedParams& p, const SeqView& v) {
   return (v.n + p.item_tokens - 1) / p.item_tokens;
 }
-// Keys that some row among the first t tokens of the sequence sees.
+// Key tiles of the prefix that each item reads before its own (p.join).
+__device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return p.join ? p.prefix_units : 0; }
+// Own keys that some row among the first t tokens of the sequence sees.
 __device__ __forceinline__ int keys_before(const PagedParams& p, int b, const SeqView& v, int t) {
   return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t)) : v.len;
 }
 __device__ __forceinline__ int item_units(const PagedParams& p, int b, const SeqView& v, int i) {
   const int t = min(v.n, (i + 1) * p.item_tokens);
-  return (keys_before(p, b, v, t) + p.key_tile - 1) / p.key_tile;
+  return prefix_tiles(p) + (keys_before(p, b, v, t) + p.key_tile - 1) / p.key_tile;
+}
+// sum over j < n of floor((a j + b) / m), for a, b >= 0: whole multiples of m come out in closed
+// form, and the rest counts lattice points under a line, which is the same sum with a and m
+// exchanged and fewer terms (the steps of Euclid's algorithm on a and m).
+// Every value stays below 2^32: rows and keys of a sequence do.
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  long long s = 0;
+  for (;;) {
+    s += static_cast<long long>(a / m) * (static_cast<long long>(n) * (n - 1) / 2) +
+         static_cast<long long>(b / m) * n;
+    a %= m;
+    b %= m;
+    const uint32_t top = a * n + b;
+    if (top < m) return s;
+    n = top / m;
+    b = top % m;
+    const uint32_t x = a;
+    a = m;
+    m = x;
+  }
 }
 // Units of a sequence's items [0, i) for one head.
 __device__ __forceinline__ long long units_before(const PagedParams& p, int b, const SeqView& v, int i) {
+  if (i <= 0) return 0;
   if (b < 0 || !p.causal) return static_cast<long long>(i) * item_units(p, b, v, 0);
-  long long s = 0;
-  for (int j = 0; j < i; ++j) s += item_units(p, b, v, j);
+  // items before the last see len - n + (j + 1) item_tokens keys, none while that is negative
+  const int whole = min(i, seq_items(p, v) - 1);
+  const int it = p.item_tokens, first = v.len - v.n;
+  const int skip = first < 0 ? min(whole, -first / it) : 0;
+  long long s = static_cast<long long>(i) * prefix_tiles(p);
+  if (whole > skip) s += floor_sum(whole - skip, p.key_tile, it, first + (skip + 1) * it + p.key_tile - 1);
+  if (i > whole) s += (v.len + p.key_tile - 1) / p.key_tile;
   return s;
 }
 __device__ __forceinline__ long long head_units(const PagedParams& p, int b, const SeqView& v) {
@@ -106,24 +136,40 @@ __device__ __forceinline__ long long head_units(const PagedParams& p, int b, con
 struct Segment {
   int b, h, i;                  // sequence, KV head, item
   SeqView v;
-  int k0, k1;                   // key tiles [k0, k1) of the item
+  int k0, k1, nk;               // key tiles [k0, k1) of the item's nk
+  bool two;                     // the item has two tiles of query tokens
 };
+// Key tile kt of an item: the sequence whose pages hold it (-1: the prefix), its first key there
+// and that sequence's keys.
+struct KeyTile {
+  int b, key0, len;
+};
+__device__ __forceinline__ KeyTile key_tile_at(const PagedParams& p, const Segment& g, int kt) {
+  const int before = prefix_tiles(p);
+  if (kt < before) return {-1, kt * p.key_tile, p.prefix_tokens};
+  return {g.b, (kt - before) * p.key_tile, g.v.len};
+}
 struct Walk {
   long long u, u1;              // units left
   long long item_first;         // first unit of the item (b, h, i)
   int b, h, i;
-  SeqView v;
+  SeqView v, next;              // sequence b, and b + 1 loaded ahead
   int items;
 };
+__device__ __forceinline__ void walk_to(const PagedParams& p, Walk& w, int b) {
+  w.b = b;
+  w.items = seq_items(p, w.v);
+  if (b + 1 < p.B) w.next = seq_view(p, b + 1);
+}
 
-// Block-wide: the first unit of every sequence, and this CTA's place in them. `first_of(b)`
-// gives the units of one head of sequence b. Every thread of the block calls it; s must hold
-// 2 + blockDim.x / 32 long longs. CTA 0 writes the plan.
+// Block-wide: the first unit of every sequence, and this CTA's place in them. units_of_head(b,
+// view) gives the units of one head of sequence b. Every thread of the block calls it; s must
+// hold 2 + blockDim.x / 32 long longs. CTA 0 writes the plan.
 template <typename HeadUnits>
 __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, HeadUnits&& units_of_head) {
   const int nt = blockDim.x, t = threadIdx.x;
   const int lane = t & 31, warp = t >> 5, warps = nt >> 5;
-  const int b_first = p.prefix_tokens > 0 ? -1 : 0;
+  const int b_first = p.prefix_tokens > 0 && !p.join ? -1 : 0;
   const int n_seq = p.B - b_first;
   const int per = (n_seq + nt - 1) / nt;
   const int b0 = b_first + min(n_seq, t * per), b1 = b_first + min(n_seq, (t + 1) * per);
@@ -174,15 +220,28 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
   w.u = u0;
   w.u1 = u1;
   if (u0 < u1) {
-    w.b = static_cast<int>(s[1]);
-    w.v = seq_view(p, w.b);
-    w.items = seq_items(p, w.v);
-    const long long uph = units_of_head(w.b, w.v);
+    const int b = static_cast<int>(s[1]);
+    w.v = seq_view(p, b);
+    walk_to(p, w, b);
+    const long long uph = units_of_head(b, w.v);
     w.h = static_cast<int>((u0 - s[0]) / uph);
     w.item_first = s[0] + w.h * uph;
     w.i = 0;
   }
   return w;
+}
+// To the item that holds the walk's first unit (attention; a search over the items' first units).
+__device__ __forceinline__ void walk_to_item(const PagedParams& p, Walk& w) {
+  if (w.u >= w.u1) return;
+  const long long rel = w.u - w.item_first;
+  int lo = 0, hi = w.items;                    // units_before(lo) <= rel < units_before(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (units_before(p, w.b, w.v, mid) <= rel) lo = mid;
+    else hi = mid;
+  }
+  w.item_first += units_before(p, w.b, w.v, lo);
+  w.i = lo;
 }
 
 // The next piece of one item in the CTA's units (attention: units are key tiles of items).
@@ -192,9 +251,8 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segm
       w.i = 0;
       if (++w.h >= p.Hkv) {
         w.h = 0;
-        ++w.b;
-        w.v = seq_view(p, w.b);
-        w.items = seq_items(p, w.v);
+        w.v = w.next;
+        walk_to(p, w, w.b + 1);
       }
       continue;
     }
@@ -210,10 +268,50 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segm
     g.v = w.v;
     g.k0 = static_cast<int>(w.u - w.item_first);
     g.k1 = static_cast<int>(min(static_cast<long long>(nk), w.u1 - w.item_first));
+    g.nk = nk;
+    g.two = w.v.n - w.i * p.item_tokens > p.tile_tokens;
     w.u = w.item_first + g.k1;
     return true;
   }
   return false;
+}
+
+// Segments handed from the warp that walks the schedule to the others of its CTA.
+constexpr int kRing = 8;
+struct SegmentRing {
+  uint64_t full[kRing], empty[kRing];
+  int4 a[kRing], b[kRing], c[kRing];
+};
+__device__ __forceinline__ void ring_init(SegmentRing& r, int readers) {
+  for (int i = 0; i < kRing; ++i) {
+    mbar_init(&r.full[i], 1);
+    mbar_init(&r.empty[i], readers);
+  }
+}
+// The k-th segment into the ring (one thread).
+__device__ __forceinline__ bool ring_put(SegmentRing& r, int k, const Segment& g, volatile int* abort, int* err) {
+  const int i = k % kRing;
+  if (k >= kRing && !mbar_wait_bounded(&r.empty[i], ((k / kRing) - 1) & 1, abort, err)) return false;
+  r.a[i] = make_int4(g.b, g.h, g.i, g.two);
+  r.b[i] = make_int4(g.v.r0, g.v.n, g.v.len, g.nk);
+  r.c[i] = make_int4(g.k0, g.k1, 0, 0);
+  mbar_arrive(&r.full[i]);
+  return true;
+}
+__device__ __forceinline__ Segment ring_peek(const SegmentRing& r, int k) {
+  const int i = k % kRing;
+  const int4 a = r.a[i], b = r.b[i], c = r.c[i];
+  return {a.x, a.y, a.z, {b.x, b.y, b.z}, c.x, c.y, b.w, a.w != 0};
+}
+// The k-th segment out of it (a warp; the same answer in every lane).
+__device__ __forceinline__ bool ring_take(SegmentRing& r, int k, Segment& g, volatile int* abort, int* err) {
+  const int i = k % kRing;
+  const bool ok = mbar_wait_bounded(&r.full[i], (k / kRing) & 1, abort, err);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  g = ring_peek(r, k);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[i]);
+  return true;
 }
 
 // Physical page of key `slot` of sequence b; -1 (and an error) when the table names none.
@@ -237,16 +335,23 @@ __device__ __forceinline__ int key_limit(const PagedParams& p, int b, const SeqV
   return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t + 1)) : v.len;
 }
 
-// Partial slots. Row slots: [prefix or own][stream][row][query head]; CTA slots after them.
-__host__ __device__ __forceinline__ long long row_slots(long long rows, int Hq, int streams, bool prefix) {
-  return (prefix ? 2LL : 1LL) * streams * rows * Hq;
+// Parts of a row's keys: the prefix and its own, or both in one.
+__host__ __device__ __forceinline__ int parts_of(const PagedParams& p) { return p.prefix_tokens > 0 && !p.join ? 2 : 1; }
+// Partial slots. Row slots: [part][stream][row][query head]; CTA slots after them.
+__host__ __device__ __forceinline__ long long row_slots(const PagedParams& p) {
+  return static_cast<long long>(parts_of(p)) * p.streams * p.rows * p.Hq;
 }
 __device__ __forceinline__ long long row_slot(const PagedParams& p, int b, int stream, int row, int hq) {
-  const int part = p.prefix_tokens > 0 && b >= 0 ? 1 : 0;
+  const int part = parts_of(p) == 2 && b >= 0 ? 1 : 0;
   return ((static_cast<long long>(part) * p.streams + stream) * p.rows + row) * p.Hq + hq;
 }
 __device__ __forceinline__ long long cta_slot(const PagedParams& p, int cta, int r) {
-  return row_slots(p.rows, p.Hq, p.streams, p.prefix_tokens > 0) + static_cast<long long>(cta) * p.slot_rows + r;
+  return row_slots(p) + static_cast<long long>(cta) * p.slot_rows + r;
+}
+// Whether an item's rows are written to O by the CTA that has all of its keys: two tiles (a
+// stream each) or one stream, and no other part.
+__device__ __forceinline__ bool writes_rows(const PagedParams& p, const SeqView& v, int item) {
+  return parts_of(p) == 1 && (p.streams == 1 || v.n - item * p.item_tokens > p.tile_tokens);
 }
 
 // Sequence whose rows hold `row` (row_start[b] <= row < row_start[b + 1]), or -1; warp-wide.
@@ -256,7 +361,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* row_start, int B, in
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = lane * step;
-    const bool le = at < n && row_start[lo + at] <= row;
+    const bool le = at < n && __ldcg(row_start + lo + at) <= row;
     const unsigned m = __ballot_sync(0xffffffffu, le);
     if (m == 0) return -1;
     const int k = 31 - __clz(m);
@@ -264,7 +369,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* row_start, int B, in
     n = min(step, n - k * step);
   }
   if (lo >= B) return -1;
-  return row_start[lo] <= row && row < row_start[lo + 1] ? lo : -1;
+  return __ldcg(row_start + lo) <= row && row < __ldcg(row_start + lo + 1) ? lo : -1;
 }
 
 // Weights: a unit is one key block (key_tile keys of a sequence, one KV head) with one tile of
@@ -285,8 +390,8 @@ __device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& 
       w.item_first += uph;
       if (++w.h >= p.Hkv) {
         w.h = 0;
-        ++w.b;
-        w.v = seq_view(p, w.b);
+        w.v = w.next;
+        walk_to(p, w, w.b + 1);
       }
       continue;
     }
@@ -306,8 +411,8 @@ __device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& 
 
 // ------------------------------------------------------------------ launchers
 // Tensor maps of the bf16 kernels. Query rows as (dims, heads, rows), one box a 64-dim half of
-// the G heads of tile_tokens rows; pool slots as (dims, pool rows), one box a 64-dim half of a
-// page's slots (128 of them at most).
+// the G heads of tile_tokens rows; pool slots as (64 dims, 8 rows, halves, eights of rows), one
+// box a page's slots (128 of them at most).
 bool encode_rows_tmap(CUtensorMap* map, const void* rows_dev, const PagedParams& p);
 bool encode_slots_tmap(CUtensorMap* map, const void* pool, const PagedParams& p);
 

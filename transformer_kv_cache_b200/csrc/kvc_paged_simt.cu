@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
   __shared__ long long plan_s[2 + kThreads / 32];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Walk w = plan_walk(p, plan_s, [&](int b, const SeqView& v) { return head_units(p, b, v); });
+  walk_to_item(p, w);
   Segment g;
   while (next_segment(p, w, g)) {
     const int t0 = g.i * p.item_tokens;
@@ -102,19 +103,20 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
       for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
     }
     for (int kt = g.k0; kt < g.k1; ++kt) {
-      const int key0 = kt * kKT;
+      const KeyTile tile = key_tile_at(p, g, kt);
       __syncthreads();
-      load_keys<D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
-      load_keys<D, LD>(p, p.v_pool, g.b, g.h, key0, g.v.len, vs);
+      load_keys<D, LD>(p, p.k_pool, tile.b, g.h, tile.key0, tile.len, ks);
+      load_keys<D, LD>(p, p.v_pool, tile.b, g.h, tile.key0, tile.len, vs);
       __syncthreads();
       float s[RPT][4];
       dots<D, RPT, 4>(qs + ty * RPT * LD, LD, 1, ks + tx * LD, LD, 16, s);
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
         float mx = -CUDART_INF_F;
+        const int end = (tile.b == g.b ? limit[r] : tile.len) - tile.key0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[r][j] = key0 + tx + 16 * j < limit[r] ? s[r][j] * p.scale_log2 : -CUDART_INF_F;
+          s[r][j] = tx + 16 * j < end ? s[r][j] * p.scale_log2 : -CUDART_INF_F;
           mx = fmaxf(mx, s[r][j]);
         }
 #pragma unroll
@@ -162,6 +164,17 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
     for (int r = 0; r < RPT; ++r) {
       const int at = ty * RPT + r;
       if (at >= rows) continue;
+      if (g.k0 == 0 && g.k1 == g.nk && writes_rows(p, g.v, g.i)) {
+        const long long out = static_cast<long long>(g.v.r0 + t0 + at / p.G) * p.Hq + g.h * p.G + at % p.G;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        if (p.lse && tx == 0) p.lse[out] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * D + c * 64 + tx * 4) =
+              make_float4(acc[r][4 * c] * inv, acc[r][4 * c + 1] * inv, acc[r][4 * c + 2] * inv,
+                          acc[r][4 * c + 3] * inv);
+        continue;
+      }
       const long long slot = g.k0 == 0 ? row_slot(p, g.b, 0, g.v.r0 + t0 + at / p.G, g.h * p.G + at % p.G)
                                        : cta_slot(p, blockIdx.x, at);
       if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);

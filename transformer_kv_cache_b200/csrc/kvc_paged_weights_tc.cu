@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* k_s = smem;                                     // [stage][half][128 keys][128 B]
+  uint8_t* k_s = smem;                                     // [stage][8 keys][half][key][128 B]
   uint8_t* q_s = k_s + kKeyStages * C::kTileBytes;         // [stage][half][128 rows][128 B]
   float2* row_s = reinterpret_cast<float2*>(q_s + kQueryStages * C::kTileBytes);   // [stage][128] (-lse2, limit)
   Bars& bar = *reinterpret_cast<Bars*>(row_s + kQueryStages * kTile);
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int blk = min(1 << p.page_shift, kTile);
     const int blocks = kTile / blk;
-    const int my_blk = lane % blocks, my_half = lane / blocks;
-    const bool loads = lane < blocks * C::kHalves;
+    const int my_blk = lane % blocks;
+    const bool loads = lane < blocks;
     const int past = static_cast<int>((p.pool_pages * p.Hkv) << p.page_shift);
     int ek = 0, eq = 0;
     bool ok = true;
@@ -129,8 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[st], C::kTileBytes);
         __syncwarp();
         if (loads)
-          tma_load_2d(k_s + st * C::kTileBytes + my_half * (kTile * 128) + my_blk * blk * 128, &tmap_k,
-                      &bar.k_full[st], my_half * 64, row[w]);
+          tma_load_4d(k_s + st * C::kTileBytes + my_blk * blk * (D * 2), &tmap_k, &bar.k_full[st], 0, 0, 0, row[w] >> 3);
       }
       for (int t = g.t0; t < g.t1 && ok; ++t, ++eq) {
         const int st = eq % kQueryStages;
@@ -191,9 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-              const uint32_t off = (c >> 2) * (kTile * 128) + (c & 3) * 32;
-              mma_ss(tmem + (2 * w + x) * 128, sw128_desc(k_addr + ks * C::kTileBytes + off, 16, 1024),
-                     sw128_desc(q_addr + st * C::kTileBytes + off, 16, 1024), idesc, c > 0 ? 1u : 0u);
+              mma_ss(tmem + (2 * w + x) * 128,
+                     sw128_desc(k_addr + ks * C::kTileBytes + (c >> 2) * 1024 + (c & 3) * 32, 16, C::kHalves * 1024),
+                     sw128_desc(q_addr + st * C::kTileBytes + (c >> 2) * (kTile * 128) + (c & 3) * 32, 16, 1024), idesc,
+                     c > 0 ? 1u : 0u);
             }
             mma_commit(&bar.s_full[w][x]);
             if (t + 1 == g.t1) mma_commit(&bar.k_empty[ks]);
