@@ -10,47 +10,75 @@
 // A CTA (one per SM) takes blocks of 256 keys of one KV head, a tile of 128 keys for each of
 // two streams, and runs the sequence's query tiles past them (units of kvc_paged.cuh, query tiles
 // fastest). A stream has two S^T buffers in TMEM (4 x 128 columns), so that its next product
-// runs under this one's exponentials.
+// runs under this one's exponentials. A sequence whose rows fit one tile keeps it in shared memory
+// from key block to key block.
 //
-// Roles (320 threads): warps 0-3 and 4-7 exponentials and sums of stream 0 and 1 (thread = key);
-// warp 8 issues the MMAs (both operands in shared memory); warp 9 loads by TMA: key tiles into
-// a ring of their own, query tiles into another; the rows' log2-sum-exp and last visible key go
-// beside the query tile by plain stores.
-#include "kvc_attn_common.cuh"
+// Roles (384 threads): warp 3 walks the schedule and hands out its segments through a ring;
+// warp 0 loads the key tiles by TMA (a page to a copy, looked up one block ahead); warp 2 loads
+// the query tiles and puts their rows' log2-sum-exp and last visible key beside them; warp 1 issues
+// the MMAs (both operands in shared memory); warps 4-7 and 8-11 are the exponentials and sums of
+// stream 0 and 1 (thread = key). A warp whose keys every row of the tile sees, which is all but the
+// last tiles of a causal call, adds without looking at the rows' limits (where a row's log-sum-exp
+// is not finite, nothing is skipped: +inf adds exactly nothing, NaN stays NaN).
 #include "kvc_paged.cuh"
+#include "kvc_paged_math.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 320;
+using namespace paged;
+
+constexpr int kThreads = 384;
 constexpr int kTile = 128;                     // keys of a stream, query rows of a tile
-constexpr int kKeyStages = 4;                  // key tiles (two to a block)
 constexpr int kQueryStages = 2;
+constexpr int kPoly8 = 3;                      // of 8 pairs, the exponentials on the FMA pipe
 
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kSmem = 1024 + (kKeyStages + kQueryStages) * kTileBytes + kQueryStages * kTile * 8 + 512;
+  static constexpr int kKeyStages = D == 128 ? 4 : 8;      // key tiles (two to a block)
+  static constexpr int kSmem = 1024 + (kKeyStages + kQueryStages) * kTileBytes + kQueryStages * kTile * 8 + 1152;
 };
 
 struct Bars {
-  uint64_t k_full[kKeyStages], k_empty[kKeyStages];
+  uint64_t k_full[8], k_empty[8];
   uint64_t q_full[kQueryStages], q_empty[kQueryStages];
   uint64_t s_full[2][2], s_empty[2][2];        // [stream][buffer]
   uint64_t drained;
+  SegmentRing ring;
+  int finite[kQueryStages];                    // 1: every row's log-sum-exp is
   uint32_t tmem;
   int abort;
   long long plan[2 + kThreads / 32];
 };
 
-// Query rows of tile t of the segment's sequence.
-__device__ __forceinline__ int tile_rows(const PagedParams& p, const WeightSegment& g, int t) {
+// Segments in the ring: i = key block, [k0, k1) = query tiles, nk = the sequence's query tiles,
+// two = the query tile is not the last segment's (one tile in all, same sequence and head).
+__device__ __forceinline__ int tile_rows(const PagedParams& p, const Segment& g, int t) {
   return min(p.tile_tokens, g.v.n - t * p.tile_tokens) * p.G;
 }
 // Key tiles of the block: 2, or 1 at the end of a sequence.
-__device__ __forceinline__ int block_tiles(const WeightSegment& g) {
-  return g.v.len - g.kb * (2 * kTile) > kTile ? 2 : 1;
+__device__ __forceinline__ int block_tiles(const Segment& g) { return g.v.len - g.i * (2 * kTile) > kTile ? 2 : 1; }
+
+// The walk of a consumer of query tiles through the ring's segments: a tile that stays (nk == 1)
+// is given back when the next one is due, any other after its use.
+struct QueryWalk {
+  int eq = -1;                                 // tile in use
+  bool held = false;                           // it was kept
+};
+
+// Sums of 2^(c s + y) over 32 columns that the thread's key is seen by: sum0 and sum1 gain.
+__device__ __forceinline__ void add_all(const uint32_t (&s)[32], const float* y, uint64_t c2, uint64_t& sum0,
+                                        uint64_t& sum1) {
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(y + 2 * k);
+    const uint64_t x0 = fma2(pk2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, pk2(v.x, v.y));
+    const uint64_t x1 = fma2(pk2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])), c2, pk2(v.z, v.w));
+    sum0 = add2(sum0, (k & 7) >= 8 - kPoly8 ? exp2_pair<true>(x0) : exp2_pair_mufu(x0));
+    sum1 = add2(sum1, ((k + 1) & 7) >= 8 - kPoly8 ? exp2_pair<true>(x1) : exp2_pair_mufu(x1));
+  }
 }
 
 template <int D>
@@ -63,15 +91,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* k_s = smem;                                     // [stage][8 keys][half][key][128 B]
-  uint8_t* q_s = k_s + kKeyStages * C::kTileBytes;         // [stage][half][128 rows][128 B]
-  float2* row_s = reinterpret_cast<float2*>(q_s + kQueryStages * C::kTileBytes);   // [stage][128] (-lse2, limit)
-  Bars& bar = *reinterpret_cast<Bars*>(row_s + kQueryStages * kTile);
-  static_assert(sizeof(Bars) <= 512, "barriers");
+  uint8_t* q_s = k_s + C::kKeyStages * C::kTileBytes;      // [stage][half][128 rows][128 B]
+  float* lse_s = reinterpret_cast<float*>(q_s + kQueryStages * C::kTileBytes);   // [stage][128] -lse2
+  int* limit_s = reinterpret_cast<int*>(lse_s + kQueryStages * kTile);           // [stage][128] keys that the row sees
+  Bars& bar = *reinterpret_cast<Bars*>(limit_s + kQueryStages * kTile);
+  static_assert(sizeof(Bars) <= 1152, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bar.abort;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKeyStages; ++i) {
+    for (int i = 0; i < C::kKeyStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
       mbar_init(&bar.k_empty[i], 1);
     }
@@ -84,11 +113,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.s_empty[i >> 1][i & 1], 4);
     }
     mbar_init(&bar.drained, 1);
+    ring_init(bar.ring, 11);                   // every warp but the one that fills it
     bar.abort = 0;
     mbar_fence_init();
     p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (warp == 8) {
+  if (warp == 1) {
     tmem_alloc(&bar.tmem, 512);
     tmem_relinquish();
   }
@@ -97,112 +127,182 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;              // S^T buffer x of stream w: columns (2 w + x) * 128
-  WeightSegment g;
 
-  if (warp == 9) {
-    // ------------------------------------------------------------------ producer
+  if (warp == 3) {
+    // ------------------------------------------------------------------ schedule
     if (lane == 0) {
-      tma_prefetch_desc(&tmap_q);
-      tma_prefetch_desc(&tmap_k);
-    }
-    const int blk = min(1 << p.page_shift, kTile);
-    const int blocks = kTile / blk;
-    const int my_blk = lane % blocks;
-    const bool loads = lane < blocks;
-    const int past = static_cast<int>((p.pool_pages * p.Hkv) << p.page_shift);
-    int ek = 0, eq = 0;
-    bool ok = true;
-    while (ok && next_weight_segment(p, walk, g)) {
-      const int key0 = g.kb * 2 * kTile;
-      const int nt = block_tiles(g);
-      int row[2];
-      for (int w = 0; w < nt; ++w) {
-        const int key = key0 + w * kTile + my_blk * blk;
-        const long long r = loads && key < g.v.len ? pool_row(p, g.b, g.h, key) : -1;
-        row[w] = r < 0 ? past : static_cast<int>(r);
+      bool ok = true, more = true;
+      int last_b = -1, last_h = -1;
+      for (int put = 0; ok && more; ++put) {
+        WeightSegment w{};
+        more = next_weight_segment(p, walk, w);
+        Segment g{};                           // the last one handed out has no query tiles
+        if (more) {
+          const int tiles = (w.v.n + p.tile_tokens - 1) / p.tile_tokens;
+          g = {w.b, w.h, w.kb, w.v, w.t0, w.t1, tiles, tiles > 1 || w.b != last_b || w.h != last_h};
+          last_b = w.b;
+          last_h = w.h;
+        }
+        ok = ring_put(bar.ring, put, g, abort, p.err);
       }
-      for (int w = 0; w < nt && ok; ++w, ++ek) {
-        const int st = ek % kKeyStages;
-        ok = ek < kKeyStages || mbar_wait_bounded(&bar.k_empty[st], ((ek / kKeyStages) - 1) & 1, abort, p.err);
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ keys
+    if (lane == 0) tma_prefetch_desc(&tmap_k);
+    const int blk = min(1 << p.page_shift, kTile);
+    const int blocks = kTile / blk;                        // boxes of a tile, two lanes for each of a block's
+    const int past = static_cast<int>((p.pool_pages * p.Hkv) << p.page_shift);
+    const bool leader = elect_one();
+    int ek = 0, sg = 0;
+    bool ok = true;
+    struct Box {
+      int page, key, tiles, h;
+    };
+    auto box_of = [&](const Segment& g) {
+      const int key = g.i * (2 * kTile) + lane * blk;
+      Box b{-1, key, block_tiles(g), g.h};
+      if (lane < 2 * blocks && key < g.v.len)
+        b.page = __ldg(p.page_table + static_cast<long long>(g.b) * p.max_pages + (key >> p.page_shift));
+      else
+        b.key = -1;
+      return b;
+    };
+    Segment g;
+    ok = ring_take(bar.ring, sg++, g, abort, p.err);
+    bool more = ok && g.nk > 0;
+    Box next = more ? box_of(g) : Box{-1, -1, 0, 0};
+    while (ok && more) {
+      const Box box = next;
+      ok = ring_take(bar.ring, sg++, g, abort, p.err);
+      if (!ok) break;
+      more = g.nk > 0;
+      if (more) next = box_of(g);
+      int row = past;
+      if (box.key >= 0) {
+        if (box.page < 0 || box.page >= p.pool_pages) latch_error(p.err, DERR_BOUNDS);
+        else row = ((box.page * p.Hkv + box.h) << p.page_shift) + (box.key & ((1 << p.page_shift) - 1));
+      }
+      for (int w = 0; w < box.tiles; ++w, ++ek) {
+        const int st = ek % C::kKeyStages;
+        ok = ek < C::kKeyStages || mbar_wait_bounded(&bar.k_empty[st], ((ek / C::kKeyStages) - 1) & 1, abort, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[st], C::kTileBytes);
+        int rows[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rows[i] = __shfl_sync(0xffffffffu, row, w * blocks + i);
+        if (leader) {
+          mbar_arrive_expect_tx(&bar.k_full[st], C::kTileBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < blocks)
+              tma_load_4d(k_s + st * C::kTileBytes + i * blk * (D * 2), &tmap_k, &bar.k_full[st], 0, 0, 0, rows[i] >> 3);
+        }
         __syncwarp();
-        if (loads)
-          tma_load_4d(k_s + st * C::kTileBytes + my_blk * blk * (D * 2), &tmap_k, &bar.k_full[st], 0, 0, 0, row[w] >> 3);
       }
-      for (int t = g.t0; t < g.t1 && ok; ++t, ++eq) {
+    }
+    if (lane == 0)
+      for (int i = max(0, ek - C::kKeyStages); i < ek; ++i)
+        mbar_wait_drain(&bar.k_full[i % C::kKeyStages], (i / C::kKeyStages) & 1, p.err);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ queries and their statistics
+    if (lane == 0) tma_prefetch_desc(&tmap_q);
+    int eq = 0;
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      Segment g;
+      ok = ring_take(bar.ring, sg, g, abort, p.err);
+      if (!ok || g.nk == 0) break;
+      if (!g.two) continue;
+      for (int t = g.k0; t < g.k1 && ok; ++t, ++eq) {
         const int st = eq % kQueryStages;
         const int tok0 = t * p.tile_tokens, rows = tile_rows(p, g, t);
+        float y[4];                            // loaded before the wait for the stage
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          y[i] = 0.f;
+          if (r < rows)
+            y[i] = __ldg(p.lse + static_cast<long long>(g.v.r0 + tok0 + r / p.G) * p.Hq + g.h * p.G + r % p.G);
+        }
         ok = eq < kQueryStages || mbar_wait_bounded(&bar.q_empty[st], ((eq / kQueryStages) - 1) & 1, abort, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane < C::kHalves) {
-          if (lane == 0) mbar_arrive_expect_tx(&bar.q_full[st], C::kHalves * p.tile_tokens * p.G * 128);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.q_full[st], C::kHalves * p.tile_tokens * p.G * 128);
+          for (int c = 0; c < C::kHalves; ++c)
+            tma_load_3d(q_s + st * C::kTileBytes + c * (kTile * 128), &tmap_q, &bar.q_full[st], c * 64, g.h * p.G,
+                        g.v.r0 + tok0);
         }
-        __syncwarp();
-        if (lane < C::kHalves)
-          tma_load_3d(q_s + st * C::kTileBytes + lane * (kTile * 128), &tmap_q, &bar.q_full[st], lane * 64, g.h * p.G,
-                      g.v.r0 + tok0);
-        for (int r = lane; r < kTile; r += 32) {
-          float2 x = make_float2(0.f, 0.f);    // no key is below 0: nothing is added
-          if (r < rows) {
-            const int tok = tok0 + r / p.G;
-            x.x = -1.4426950408889634f *
-                  __ldg(p.lse + static_cast<long long>(g.v.r0 + tok) * p.Hq + g.h * p.G + r % p.G);
-            x.y = __int_as_float(key_limit(p, g.b, g.v, tok));
-          }
-          row_s[st * kTile + r] = x;
+        const bool fin = __all_sync(0xffffffffu, isfinite(y[0]) && isfinite(y[1]) && isfinite(y[2]) && isfinite(y[3]));
+        if (lane == 0) bar.finite[st] = fin;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          lse_s[st * kTile + r] = -1.4426950408889634f * y[i];
+          limit_s[st * kTile + r] = r < rows ? key_limit(p, g.b, g.v, tok0 + r / p.G) : 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[st]);
       }
     }
-    if (lane == 0) {
-      for (int i = max(0, ek - kKeyStages); i < ek; ++i)
-        mbar_wait_drain(&bar.k_full[i % kKeyStages], (i / kKeyStages) & 1, p.err);
+    if (lane == 0)
       for (int i = max(0, eq - kQueryStages); i < eq; ++i)
         mbar_wait_drain(&bar.q_full[i % kQueryStages], (i / kQueryStages) & 1, p.err);
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------------ MMA issuer
-    const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(k_s);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ products
+    const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
+    const uint64_t k_desc = sw128_desc(smem_u32(k_s), 16, C::kHalves * 1024);
     const bool leader = elect_one();
-    int ek = 0, eq = 0;
+    int ek = 0;
     int steps[2] = {0, 0};
+    QueryWalk q;
     bool ok = true;
-    while (ok && next_weight_segment(p, walk, g)) {
+    for (int sg = 0; ok; ++sg) {
+      Segment g;
+      ok = ring_take(bar.ring, sg, g, abort, p.err);
+      if (!ok || g.nk == 0) break;
       const int nt = block_tiles(g);
-      for (int t = g.t0; t < g.t1 && ok; ++t, ++eq) {
-        const int st = eq % kQueryStages;
+      if (g.two && q.held) {
+        if (leader) mma_commit(&bar.q_empty[q.eq % kQueryStages]);
+        __syncwarp();
+        q.held = false;
+      }
+      for (int t = g.k0; t < g.k1 && ok; ++t) {
+        bool r = true;
+        if (g.two) {
+          ++q.eq;
+          r = mbar_wait_bounded(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort, p.err);
+        }
+        const int st = q.eq % kQueryStages;
         const int cols = (tile_rows(p, g, t) + 15) & ~15;
-        const uint32_t idesc = idesc_f16kind(1, kTile, 16, 0, 0) + (static_cast<uint32_t>(cols - 16) >> 3 << 17);
-        ok = mbar_wait_bounded(&bar.q_full[st], (eq / kQueryStages) & 1, abort, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        for (int w = 0; w < nt && ok; ++w) {
-          const int ks = (ek + w) % kKeyStages, x = steps[w] & 1;
-          if (t == g.t0) ok = mbar_wait_bounded(&bar.k_full[ks], ((ek + w) / kKeyStages) & 1, abort, p.err);
-          if (steps[w] >= 2) ok = ok && mbar_wait_bounded(&bar.s_empty[w][x], ((steps[w] >> 1) - 1) & 1, abort, p.err);
-          ok = __all_sync(0xffffffffu, ok);
+        const uint32_t idesc = idesc_f16kind(1, kTile, 16, 0, 0) + ((static_cast<uint32_t>(cols - 16) >> 3) << 17);
+        for (int w = 0; w < nt; ++w) {
+          const int ks = (ek + w) % C::kKeyStages, x = steps[w] & 1;
+          if (t == g.k0) r = r && mbar_wait_bounded(&bar.k_full[ks], ((ek + w) / C::kKeyStages) & 1, abort, p.err);
+          if (steps[w] >= 2) r = r && mbar_wait_bounded(&bar.s_empty[w][x], ((steps[w] >> 1) - 1) & 1, abort, p.err);
+          ok = __all_sync(0xffffffffu, r);
           if (!ok) break;
           ++steps[w];
           tc_fence_after();
           if (leader) {
+            // addresses stay below 2^18: an offset adds to the descriptor's address field
+            const uint64_t kd = k_desc + (ks * C::kTileBytes >> 4), qd = q_desc + (st * C::kTileBytes >> 4);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              mma_ss(tmem + (2 * w + x) * 128,
-                     sw128_desc(k_addr + ks * C::kTileBytes + (c >> 2) * 1024 + (c & 3) * 32, 16, C::kHalves * 1024),
-                     sw128_desc(q_addr + st * C::kTileBytes + (c >> 2) * (kTile * 128) + (c & 3) * 32, 16, 1024), idesc,
-                     c > 0 ? 1u : 0u);
-            }
+            for (int c = 0; c < D / 16; ++c)
+              mma_ss(tmem + (2 * w + x) * 128, kd + (((c >> 2) * 1024 + (c & 3) * 32) >> 4),
+                     qd + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4), idesc, c > 0 ? 1u : 0u);
             mma_commit(&bar.s_full[w][x]);
-            if (t + 1 == g.t1) mma_commit(&bar.k_empty[ks]);
+            if (t + 1 == g.k1) mma_commit(&bar.k_empty[ks]);
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (leader) mma_commit(&bar.q_empty[st]);
-        __syncwarp();
+        if (g.nk > 1) {
+          if (leader) mma_commit(&bar.q_empty[st]);
+          __syncwarp();
+        } else {
+          q.held = true;
+        }
       }
       ek += nt;
     }
@@ -211,18 +311,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_drain(&bar.drained, 0, p.err);
   } else {
     // ------------------------------------------------------------------ sums of stream w
-    const int w = warp >> 2, wq = warp & 3;
+    const int w = (warp - 4) >> 2, wq = warp & 3;
     const uint32_t s_col = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 2 * w * 128;
     const float c = p.scale_log2;
-    int steps = 0, eq = 0;
+    const uint64_t c2 = pk2(c, c);
+    int steps = 0;
+    QueryWalk q;
     bool ok = true;
-    while (ok && next_weight_segment(p, walk, g)) {
+    for (int sg = 0; ok; ++sg) {
+      Segment g;
+      ok = ring_take(bar.ring, sg, g, abort, p.err);
+      if (!ok || g.nk == 0) break;
       const bool mine = w < block_tiles(g);
-      const int key = g.kb * 2 * kTile + w * kTile + wq * 32 + lane;
+      const int key0 = g.i * 2 * kTile + w * kTile + wq * 32, key = key0 + lane;
+      if (g.two && q.held) {
+        if (lane == 0) mbar_arrive(&bar.q_empty[q.eq % kQueryStages]);
+        q.held = false;
+      }
       float total = 0.f;
-      for (int t = g.t0; t < g.t1 && ok; ++t, ++eq) {
-        const int st = eq % kQueryStages;
-        ok = mbar_wait_bounded(&bar.q_full[st], (eq / kQueryStages) & 1, abort, p.err);   // the statistics
+      for (int t = g.k0; t < g.k1; ++t) {
+        if (g.two) {
+          ++q.eq;
+          ok = mbar_wait_bounded(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort, p.err);
+        }
+        const int st = q.eq % kQueryStages;
         if (mine) {
           const int rows = tile_rows(p, g, t);
           const int x = steps & 1;
@@ -231,32 +343,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++steps;
           tc_fence_after();
-          const float2* st_row = row_s + st * kTile;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int q = 0; q < rows; q += 32) {
-            uint32_t s[32];
-            tmem_ld32(s_col + x * 128 + q, s);
+          const uint32_t buf = s_col + x * 128;
+          const float* y = lse_s + st * kTile;
+          const int* limit = limit_s + st * kTile;
+          // rows see more keys the later they are: the first one's limit is the tile's least
+          const bool all = bar.finite[st] && min(key0 + 31, g.v.len - 1) < limit[0];
+          float rest = 0.f;
+          uint64_t sum0 = 0, sum1 = 0;
+          int done = 0;
+          if (all && rows >= 32) {
+            uint32_t a[32], b[32];             // the next columns arrive under these ones' exponentials
+            tmem_ld32(buf, a);
+            tmem_ld_wait();
+            for (;; done += 64) {
+              const bool second = done + 64 <= rows;
+              if (second) tmem_ld32(buf + done + 32, b);
+              add_all(a, y + done, c2, sum0, sum1);
+              if (!second) {
+                done += 32;
+                break;
+              }
+              tmem_ld_wait();
+              const bool third = done + 96 <= rows;
+              if (third) tmem_ld32(buf + done + 64, a);
+              add_all(b, y + done + 32, c2, sum0, sum1);
+              if (!third) {
+                done += 64;
+                break;
+              }
+              tmem_ld_wait();
+            }
+          }
+          for (; done < rows; done += 16) {
+            uint32_t s[16];
+            tmem_ld16(buf + done, s);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 y = st_row[q + k];
-              const float e = ex2(fmaf(__uint_as_float(s[k]), c, y.x));
-              sum[k & 3] += key < __float_as_int(y.y) ? e : 0.f;
-            }
+            for (int k = 0; k < 16; ++k)
+              if (done + k < rows && key < limit[done + k])
+                rest += ex2(fmaf(__uint_as_float(s[k]), c, y[done + k]));
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.s_empty[w][x]);
-          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float e0, e1;
+          up2(add2(sum0, sum1), e0, e1);
+          total += (e0 + e1) + rest;
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&bar.q_empty[st]);
+        if (g.nk > 1) {
+          if (lane == 0) mbar_arrive(&bar.q_empty[st]);
+        } else {
+          q.held = true;
+        }
       }
       if (!ok) break;
-      if (g.t0 > 0) {
+      if (g.k0 > 0) {
         p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + w * kTile + wq * 32 + lane] = total;
-        if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.kb, 1);
+        if (warp == 4 && lane == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.i, 1);
       } else if (key < g.v.len) {
         p.scores[(static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key] += total;
       }
@@ -264,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
