@@ -484,8 +484,8 @@ typedef struct {
   const int32_t* prefix_pages;  /* [ceil(prefix_tokens / page_size)] or NULL */
   int32_t* next_positions;      /* [num_seqs] position of the next token appended, or NULL */
   float* scores;                /* [num_seqs][num_kv_heads][max_pages * page_size] accumulated weight
-                                   of the token in each slot, or NULL */
-  int32_t* positions;           /* same shape: position of the token in each slot, or NULL */
+                                   of the token in each slot, 16-byte aligned, or NULL */
+  int32_t* positions;           /* same shape: position of the token in each slot, 16-byte aligned, or NULL */
   int32_t* error;               /* one word, or NULL: set from 0 by the first device-side failure: 1 a
                                    bounded wait gave up, 2 no room for an append, 3 a length, row
                                    or page out of range */

@@ -426,19 +426,19 @@ def kvc_attend_paged_noalloc(q, o, k_pool, v_pool, pool_pages: int, page_table, 
 
 # ---------------------------------------------------------------- paged batches
 
-def _same_device(what, x, device, dtype=None, shape=None):
-    """A CUDA tensor of the batch's device (and type and shape), packed densely."""
-    if not getattr(x, "is_cuda", False):
-        raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
-    if x.device != device:
-        raise ValueError(f"{what} is on {x.device}, the batch on {device}")
-    if dtype is not None and x.dtype != dtype:
-        raise TypeError(f"{what} is {x.dtype}, not {dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(x.shape)}, not {tuple(shape)}")
-    if not x.is_contiguous():
+def _packed(what, x, device, dtype, shape):
+    """The pointer of a densely packed CUDA tensor of the batch's device, of this type and shape."""
+    if x.device != device or x.dtype != dtype or x.shape != shape or not x.is_contiguous():
+        if not getattr(x, "is_cuda", False):
+            raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
+        if x.device != device:
+            raise ValueError(f"{what} is on {x.device}, the batch on {device}")
+        if x.dtype != dtype:
+            raise TypeError(f"{what} is {x.dtype}, not {dtype}")
+        if x.shape != shape:
+            raise ValueError(f"{what} has shape {tuple(x.shape)}, not {tuple(shape)}")
         raise ValueError(f"{what} must be contiguous")
-    return x
+    return x.data_ptr()
 
 
 def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, softmax_scale: float, *,
@@ -452,83 +452,79 @@ def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, soft
     dev, i32 = k_pool.device, torch.int32
     if k_pool.dtype not in types or k_pool.dim() != 4:
         raise TypeError("k_pool must be a 4-dimensional float32 or bfloat16 tensor")
-    _same_device("k_pool", k_pool, dev)
-    _same_device("v_pool", v_pool, dev, k_pool.dtype, k_pool.shape)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [sequences, pages]")
     n, max_pages = page_table.shape
     pool_pages, heads, page, dim = k_pool.shape
-    _same_device("page_table", page_table, dev, i32)
-    _same_device("lengths", lengths, dev, i32, (n,))
-    if prefix_pages is not None:
-        _same_device("prefix_pages", prefix_pages, dev, i32)
-    if prefix_tokens > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_tokens):
-        raise ValueError("prefix_pages must hold prefix_tokens tokens")
-    if next_positions is not None:
-        _same_device("next_positions", next_positions, dev, i32, (n,))
-    if scores is not None:
-        _same_device("scores", scores, dev, torch.float32, (n, heads, max_pages * page))
-    if positions is not None:
-        _same_device("positions", positions, dev, i32, (n, heads, max_pages * page))
-    if error is not None:
-        _same_device("error", error, dev, i32)
-        if error.numel() < 1:
-            raise ValueError("error must hold one word")
+    slots = (n, heads, max_pages * page)
     b = kvc_paged_batch()
     b.dtype, b.num_seqs, b.num_q_heads, b.num_kv_heads = types[k_pool.dtype], n, num_q_heads, heads
     b.head_dim, b.page_size, b.max_pages, b.prefix_tokens = dim, page, max_pages, prefix_tokens
     b.pool_pages, b.softmax_scale = pool_pages, softmax_scale
-    held = dict(k_pool=k_pool, v_pool=v_pool, page_table=page_table, lengths=lengths, prefix_pages=prefix_pages,
-                next_positions=next_positions, scores=scores, positions=positions, error=error)
-    for name, x in held.items():
-        setattr(b, name, None if x is None else x.data_ptr())
-    b._tensors, b._device, b._dtype = held, dev, k_pool.dtype
+    held = dict(k_pool=(k_pool, k_pool.dtype, k_pool.shape), v_pool=(v_pool, k_pool.dtype, k_pool.shape),
+                page_table=(page_table, i32, (n, max_pages)), lengths=(lengths, i32, (n,)),
+                next_positions=(next_positions, i32, (n,)), scores=(scores, torch.float32, slots),
+                positions=(positions, i32, slots))
+    if prefix_pages is not None:
+        held["prefix_pages"] = prefix_pages, i32, (prefix_pages.numel(),)
+    if prefix_tokens > 0 and (prefix_pages is None or prefix_pages.numel() * page < prefix_tokens):
+        raise ValueError("prefix_pages must hold prefix_tokens tokens")
+    if error is not None:
+        if error.numel() < 1:
+            raise ValueError("error must hold one word")
+        held["error"] = error, i32, error.shape
+    for name, (x, dtype, shape) in held.items():
+        setattr(b, name, None if x is None else _packed(name, x, dev, dtype, shape))
+    # what the calls below check against, and the tensors, which the struct keeps alive
+    b._torch, b._device, b._index, b._dtype = torch, dev, dev.index, k_pool.dtype
+    b._q_heads, b._kv_heads, b._dim, b._rows_shape = num_q_heads, heads, dim, (n + 1,)
+    # torch's own accessor of the current stream's handle (building a Stream object costs 3 us)
+    b._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    b._ref, b._tensors = ctypes.byref(b), [x for x, _, _ in held.values()]
     return b
 
 
 def _paged_rows(batch, what, x, heads):
     """(pointer, row stride, rows) of a [rows, heads, head dim] tensor whose rows are packed."""
-    if not getattr(x, "is_cuda", False):
-        raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
     if x.device != batch._device or x.dtype != batch._dtype:
+        if not getattr(x, "is_cuda", False):
+            raise TypeError(f"{what}: a CUDA tensor is expected here, not a host buffer")
         raise ValueError(f"{what} is {x.dtype} on {x.device}, the batch {batch._dtype} on {batch._device}")
-    d = batch.head_dim
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or x.stride(2) != 1 or \
-            (heads > 1 and x.stride(1) != d):
+    shape, d = x.shape, batch._dim
+    stride = x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{what} must be [rows, {heads}, {d}] with packed rows")
-    rows = x.shape[0]
-    return x.data_ptr(), (x.stride(0) if rows > 1 else heads * d), rows
+    rows = shape[0]
+    return x.data_ptr(), (stride[0] if rows > 1 else heads * d), rows
 
 
 def _paged_call(batch, stream, fn, *args):
     """fn(batch, *args, stream) with the batch's device current; the default stream is that
     device's current one."""
-    import torch
-    if torch.cuda.current_device() == batch._device.index:
-        st = fn(ctypes.byref(batch), *args, _stream(stream))
+    cuda = batch._torch.cuda
+    if cuda.current_device() == batch._index:
+        st = fn(batch._ref, *args, batch._current_stream(batch._index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(batch._device):
-            st = fn(ctypes.byref(batch), *args, _stream(stream))
+        with cuda.device(batch._device):
+            st = fn(batch._ref, *args, _stream(stream))
     if st != 0:
         raise KVCError(st, f"{fn.__name__} failed")
 
 
 def _row_start(batch, x):
-    import torch
-    return _same_device("row_start", x, batch._device, torch.int32, (batch.num_seqs + 1,)).data_ptr()
+    return _packed("row_start", x, batch._device, batch._torch.int32, batch._rows_shape)
 
 
 def _workspace(batch, x):
-    _same_device("workspace", x, batch._device)
-    return x.data_ptr(), x.numel() * x.element_size()
+    return _packed("workspace", x, batch._device, x.dtype, x.shape), x.numel() * x.element_size()
 
 
 def kvc_paged_workspace(batch: kvc_paged_batch, rows: int, keep: int = 0) -> int:
     """Bytes of workspace for calls with up to `rows` rows and an eviction to `keep`."""
-    import torch
     n = ctypes.c_int64(0)
-    with torch.cuda.device(batch._device):
-        st = _lib.kvc_paged_workspace(ctypes.byref(batch), rows, keep, ctypes.byref(n))
+    with batch._torch.cuda.device(batch._device):
+        st = _lib.kvc_paged_workspace(batch._ref, rows, keep, ctypes.byref(n))
     if st != 0:
         raise KVCError(st, "kvc_paged_workspace failed")
     return n.value
@@ -536,8 +532,8 @@ def kvc_paged_workspace(batch: kvc_paged_batch, rows: int, keep: int = 0) -> int
 
 def kvc_paged_append(batch: kvc_paged_batch, k, v, row_start, stream=None) -> None:
     """Append k, v [rows, KV heads, head dim] (rows row_start[b] .. of sequence b)."""
-    kp, ks, rows = _paged_rows(batch, "k", k, batch.num_kv_heads)
-    vp, vs, v_rows = _paged_rows(batch, "v", v, batch.num_kv_heads)
+    kp, ks, rows = _paged_rows(batch, "k", k, batch._kv_heads)
+    vp, vs, v_rows = _paged_rows(batch, "v", v, batch._kv_heads)
     if rows != v_rows:
         raise ValueError("k and v have different numbers of rows")
     _paged_call(batch, stream, _lib.kvc_paged_append, kp, vp, ks, vs, rows, _row_start(batch, row_start))
@@ -547,25 +543,23 @@ def kvc_paged_attend(batch: kvc_paged_batch, q, o, row_start, workspace, lse=Non
                      stream=None) -> None:
     """Attention of q [rows, query heads, head dim] into o (and the log-sum-exp into lse
     [rows, query heads] fp32) over the shared prefix and the sequences' own tokens."""
-    import torch
-    qp, qs, rows = _paged_rows(batch, "q", q, batch.num_q_heads)
-    _same_device("o", o, batch._device, batch._dtype, q.shape)
+    qp, qs, rows = _paged_rows(batch, "q", q, batch._q_heads)
+    op = _packed("o", o, batch._device, batch._dtype, q.shape)
     if lse is not None:
-        _same_device("lse", lse, batch._device, torch.float32, q.shape[:2])
+        lse = _packed("lse", lse, batch._device, batch._torch.float32, (rows, batch._q_heads))
     wp, wn = _workspace(batch, workspace)
-    _paged_call(batch, stream, _lib.kvc_paged_attend, qp, qs, o.data_ptr(),
-                None if lse is None else lse.data_ptr(), rows, _row_start(batch, row_start), int(bool(causal)), wp, wn)
+    _paged_call(batch, stream, _lib.kvc_paged_attend, qp, qs, op, lse, rows, _row_start(batch, row_start),
+                1 if causal else 0, wp, wn)
 
 
 def kvc_paged_weights(batch: kvc_paged_batch, q, lse, row_start, workspace, causal: bool = True,
                       stream=None) -> None:
     """Add the attention weight that each of the sequences' own tokens receives to its score."""
-    import torch
-    qp, qs, rows = _paged_rows(batch, "q", q, batch.num_q_heads)
-    _same_device("lse", lse, batch._device, torch.float32, q.shape[:2])
+    qp, qs, rows = _paged_rows(batch, "q", q, batch._q_heads)
+    lp = _packed("lse", lse, batch._device, batch._torch.float32, (rows, batch._q_heads))
     wp, wn = _workspace(batch, workspace)
-    _paged_call(batch, stream, _lib.kvc_paged_weights, qp, qs, lse.data_ptr(), rows, _row_start(batch, row_start),
-                int(bool(causal)), wp, wn)
+    _paged_call(batch, stream, _lib.kvc_paged_weights, qp, qs, lp, rows, _row_start(batch, row_start),
+                1 if causal else 0, wp, wn)
 
 
 def kvc_paged_evict(batch: kvc_paged_batch, keep: int, sinks: int, recent: int, workspace, stream=None) -> None:

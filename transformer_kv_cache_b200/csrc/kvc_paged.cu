@@ -12,6 +12,7 @@ namespace kvc {
 namespace {
 
 constexpr int kMaxGroup = 64;                  // query heads per KV head
+constexpr int kFewRows = 8;                    // rows a sequence (on average) up to which a CTA appends them
 constexpr long long kMaxSlots = 1LL << 30;     // slots of a sequence, tokens of the prefix
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
@@ -31,7 +32,7 @@ bool valid_batch(const kvc_paged_batch* b) {
   if (b->prefix_tokens < 0 || b->prefix_tokens > kMaxSlots || (b->prefix_tokens > 0 && !b->prefix_pages)) return false;
   if (!(b->softmax_scale > 0.f) || !std::isfinite(b->softmax_scale) || b->reserved != 0) return false;
   if (!b->k_pool || !b->v_pool || !b->page_table || !b->lengths) return false;
-  return aligned16(b->k_pool) && aligned16(b->v_pool);
+  return aligned16(b->k_pool) && aligned16(b->v_pool) && aligned16(b->scores) && aligned16(b->positions);
 }
 
 int page_shift(int page_size) {
@@ -151,8 +152,12 @@ int move_cap(const kvc_paged_batch* b, int32_t keep) {
   const long long cap = static_cast<long long>(b->max_pages) * b->page_size;
   return static_cast<int>(std::min<long long>(keep, std::max<long long>(cap - keep, 0)));
 }
+size_t evict_counts_bytes(const kvc_paged_batch* b) {
+  return align256(sizeof(int32_t) * static_cast<size_t>(b->num_seqs) * b->num_kv_heads);
+}
 size_t evict_bytes(const kvc_paged_batch* b, int32_t keep) {
-  return align256(sizeof(int32_t) * 2 * static_cast<size_t>(b->num_seqs) * b->num_kv_heads * move_cap(b, keep));
+  return evict_counts_bytes(b) +
+         align256(sizeof(int2) * 2 * static_cast<size_t>(b->num_seqs) * b->num_kv_heads * move_cap(b, keep));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -172,8 +177,8 @@ struct AppendParams {
   int B, H, page_shift, max_pages, rows, row_bytes;   // row_bytes: one head's
   long long pool_pages, k_stride, v_stride;           // bytes between source rows
   const int32_t* page_table;
-  const int32_t* lengths;
-  const int32_t* next_positions;
+  int32_t* lengths;
+  int32_t* next_positions;
   const int32_t* row_start;
   const uint8_t* k;
   const uint8_t* v;
@@ -184,42 +189,15 @@ struct AppendParams {
   int* err;
 };
 
-// One warp per row, and per slot behind a sequence's last token that may need clearing: a page
-// that this call begins ends in zeros, as every page of the cache does. Bound by the copies
-// (rows in, slots out); 16 bytes a lane.
-__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int page_size = 1 << p.page_shift;
-  int b, slot = 0, row = -1;
-  if (warp < p.rows) {
-    b = find_sequence(p.row_start, p.B, warp);
-    row = warp;
-  } else {
-    const int z = warp - p.rows;
-    b = z / (page_size - 1);
-    slot = z % (page_size - 1);
-    if (b >= p.B) return;
-  }
-  if (b < 0) return;                                   // behind the last sequence
-  const int lo = p.row_start[b], hi = p.row_start[b + 1], len = p.lengths[b];
-  const int cap = p.max_pages << p.page_shift;
-  if (lo < 0 || hi < lo || hi > p.rows || len < 0 || len > cap) {
-    if (lane == 0) latch_error(p.err, DERR_BOUNDS);
-    return;
-  }
-  const int n = hi - lo;
-  if (n > cap - len) {                                 // no room: none of the sequence's rows
-    if (lane == 0) latch_error(p.err, DERR_POOL);
-    return;
-  }
-  if (row >= 0) {
-    slot = len + row - lo;
-  } else {
-    const int end = len + n;
-    const int first = end & ~(page_size - 1);          // first slot of the last page written
-    slot += end;
+// One task of a sequence (a warp): task i < n copies its i-th row, the tasks behind those clear the
+// slots behind its last token, where the call begins that page (every page of the cache ends in
+// zeros). 16 bytes a lane.
+__device__ __forceinline__ void append_task(const AppendParams& p, int b, int lo, int n, int len, int task) {
+  const int lane = threadIdx.x & 31, page_size = 1 << p.page_shift;
+  const bool copy = task < n;
+  int slot = len + task;
+  if (!copy) {
+    const int end = len + n, first = end & ~(page_size - 1);   // first slot of the last page written
     if (n == 0 || end == first || first < len || slot >= first + page_size) return;
   }
   const int32_t page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + (slot >> p.page_shift));
@@ -230,32 +208,73 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p)
   const int per_head = p.row_bytes >> 4, chunks = p.H * per_head;
   const long long head_bytes = static_cast<long long>(p.row_bytes) << p.page_shift;
   const long long base = page * p.H * head_bytes + (slot & (page_size - 1)) * static_cast<long long>(p.row_bytes);
-  const uint4* k = reinterpret_cast<const uint4*>(p.k + (row >= 0 ? row * p.k_stride : 0));
-  const uint4* v = reinterpret_cast<const uint4*>(p.v + (row >= 0 ? row * p.v_stride : 0));
+  const long long row = lo + task;
+  const uint4* k = reinterpret_cast<const uint4*>(p.k + (copy ? row * p.k_stride : 0));
+  const uint4* v = reinterpret_cast<const uint4*>(p.v + (copy ? row * p.v_stride : 0));
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
   for (int c = lane; c < chunks; c += 32) {
     const long long to = base + (c / per_head) * head_bytes + (c % per_head) * 16;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(p.k_pool + to) = row >= 0 ? __ldg(k + c) : zero;
-    *reinterpret_cast<uint4*>(p.v_pool + to) = row >= 0 ? __ldg(v + c) : zero;
+    *reinterpret_cast<uint4*>(p.k_pool + to) = copy ? __ldg(k + c) : zero;
+    *reinterpret_cast<uint4*>(p.v_pool + to) = copy ? __ldg(v + c) : zero;
   }
-  if (row < 0) return;
+  if (!copy) return;
+  const int cap = p.max_pages << p.page_shift;
+  const int position = p.positions ? p.next_positions[b] + task : 0;
   for (int h = lane; h < p.H; h += 32) {
     const long long at = (static_cast<long long>(b) * p.H + h) * cap + slot;
     if (p.scores) p.scores[at] = 0.f;
-    if (p.positions) p.positions[at] = p.next_positions[b] + row - lo;
+    if (p.positions) p.positions[at] = position;
   }
 }
+// A sequence's rows and length; false (and an error) where they are out of range or do not fit.
+__device__ __forceinline__ bool append_view(const AppendParams& p, int b, int& lo, int& n, int& len) {
+  lo = p.row_start[b];
+  const int hi = p.row_start[b + 1], cap = p.max_pages << p.page_shift;
+  len = p.lengths[b];
+  n = hi - lo;
+  const bool in = lo >= 0 && hi >= lo && hi <= p.rows && len >= 0 && len <= cap;
+  if (in && n <= cap - len) return true;
+  latch_error(p.err, in ? DERR_POOL : DERR_BOUNDS);
+  return false;
+}
+__device__ __forceinline__ void grow(const AppendParams& p, int b, int n, int len) {
+  p.lengths[b] = len + n;
+  if (p.next_positions) p.next_positions[b] += n;
+}
 
-// Lengths and next positions of the sequences that were appended to.
-__global__ void paged_grow_kernel(const int32_t* row_start, int32_t* lengths, int32_t* next_positions, int B, int rows,
-                                  int cap) {
+// A CTA per sequence, which then grows by its rows.
+__global__ void __launch_bounds__(512) paged_append_few_kernel(const AppendParams p) {
   griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x, warps = blockDim.x >> 5;
+  int lo, n, len;
+  if (!append_view(p, b, lo, n, len)) return;
+  const int tasks = n + (1 << p.page_shift) - 1;
+  for (int task = threadIdx.x >> 5; task < tasks; task += warps) append_task(p, b, lo, n, len, task);
+  __syncthreads();
+  if (threadIdx.x == 0) grow(p, b, n, len);
+}
+
+// A warp per row of the batch and per slot that may need clearing; the lengths grow in a kernel of
+// their own, once nobody reads the old ones.
+__global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, behind = (1 << p.page_shift) - 1;
+  const int z = warp - p.rows;
+  const int b = z < 0 ? find_sequence(p.row_start, p.B, warp) : z / behind;
+  if (b < 0 || b >= p.B) return;                       // behind the last sequence
+  int lo, n, len;
+  if (!append_view(p, b, lo, n, len)) return;
+  append_task(p, b, lo, n, len, z < 0 ? warp - lo : n + z % behind);
+}
+__global__ void paged_grow_kernel(const AppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= B) return;
-  const int lo = row_start[b], hi = row_start[b + 1], len = lengths[b];
-  if (lo < 0 || hi < lo || hi > rows || len < 0 || len > cap || hi - lo > cap - len) return;
-  lengths[b] = len + hi - lo;
-  if (next_positions) next_positions[b] += hi - lo;
+  int lo, n, len;
+  if (b < p.B && append_view(p, b, lo, n, len)) grow(p, b, n, len);
 }
 
 // ------------------------------------------------------------------ merging partial results
@@ -288,13 +307,18 @@ __device__ __forceinline__ Partial<D> load_partial(const PagedParams& p, long lo
   return x;
 }
 
+// x / y in 32 bits where they hold both.
+__device__ __forceinline__ int quotient(long long x, long long y) {
+  if (x >> 32 == 0) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(min(y, 0xffffffffLL)));
+  return static_cast<int>(x / y);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   constexpr int kPer = D / 32;
-  const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(warp / p.Hq), hq = static_cast<int>(warp % p.Hq);
-  const int b = row < p.rows ? find_sequence(p.row_start, p.B, row) : -1;
+  const int row = blockIdx.x, hq = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int b = hq < p.Hq ? find_sequence(p.row_start, p.B, row) : -1;
   const int h = hq / p.G, g = hq % p.G;
   const int parts = parts_of(p);
   // per part: units of the item, its first unit (without the sequence's), and the row's place
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     if (k >= parts || nk[k] == 0) continue;
     const int s = parts == 2 && k == 0 ? -1 : b;
     const long long u0 = first[k] + (s < 0 ? 0 : own);
-    const int c0 = static_cast<int>(u0 / U), c1 = static_cast<int>((u0 + nk[k] - 1) / U);
+    const int c0 = quotient(u0, U), c1 = quotient(u0 + nk[k] - 1, U);
     if (c0 == c1 && whole) return;                     // written by its CTA
     for (int c = c0; c <= c1; ++c) {
       const long long s0 = c == c0 ? row_slot(p, s, 0, row, hq)
@@ -370,8 +394,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
 
 template <typename T>
 cudaError_t launch_merge(cudaStream_t s, const PagedParams& p) {
-  const long long warps = static_cast<long long>(p.rows) * p.Hq;
-  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
+  const dim3 grid(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.Hq + 3) / 4));
   return p.D == 64 ? launch_pdl(paged_merge_kernel<T, 64>, grid, dim3(128), 0, s, p)
                    : launch_pdl(paged_merge_kernel<T, 128>, grid, dim3(128), 0, s, p);
 }
@@ -485,14 +508,13 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void*
   p.scores = batch->scores;
   p.positions = batch->positions;
   p.err = batch->error;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // few rows a sequence: one launch, a CTA for each
+  if (rows <= kFewRows * p.B) return status_of(launch_pdl(paged_append_few_kernel, dim3(p.B), dim3(512), 0, s, p));
   const long long warps = rows + static_cast<long long>(p.B) * (batch->page_size - 1);
   if (warps > INT_MAX - 8) return KVC_ERR_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e =
-      launch_pdl(paged_append_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, p);
-  if (e == cudaSuccess)
-    e = launch_pdl(paged_grow_kernel, dim3((p.B + 255) / 256), dim3(256), 0, s, row_start_dev, batch->lengths,
-                   batch->next_positions, p.B, rows, batch->max_pages * batch->page_size);
+  cudaError_t e = launch_pdl(paged_append_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, p);
+  if (e == cudaSuccess) e = launch_pdl(paged_grow_kernel, dim3((p.B + 255) / 256), dim3(256), 0, s, p);
   return status_of(e);
 }
 
@@ -585,7 +607,8 @@ extern "C" kvc_status kvc_paged_evict(const kvc_paged_batch* batch, int32_t keep
   p.v_pool = static_cast<uint8_t*>(batch->v_pool);
   p.scores = batch->scores;
   p.positions = batch->positions;
-  p.moves = static_cast<int32_t*>(workspace_dev);
+  p.counts = static_cast<int32_t*>(workspace_dev);
+  p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace_dev) + evict_counts_bytes(batch));
   p.move_cap = move_cap(batch, keep);
   p.err = batch->error;
   return status_of(launch_paged_evict(static_cast<cudaStream_t>(stream), p, batch->lengths));

@@ -431,7 +431,8 @@ struct EvictParams {
   uint8_t* v_pool;
   float* scores;
   int32_t* positions;
-  int32_t* moves;               // workspace: [B * Hkv][2][move_cap] slots moved to and from
+  int32_t* counts;              // workspace: [B * Hkv] moves, -1 where nothing is evicted
+  int2* moves;                  // workspace: [B * Hkv][2][move_cap] (slot, pool row) moved to and from
   int move_cap;
   int* err;
 };
