@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kMaxGroup = 64;                  // query heads per KV head
 constexpr int kFewRows = 8;                    // rows a sequence (on average) up to which a CTA appends them
+constexpr int kManyHeads = 8192;               // rows x heads from which on the merge packs four into a warp
 constexpr long long kMaxSlots = 1LL << 30;     // slots of a sequence, tokens of the prefix
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
@@ -278,125 +279,144 @@ __global__ void paged_grow_kernel(const AppendParams p) {
 }
 
 // ------------------------------------------------------------------ merging partial results
-// One warp per (row, query head): O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the row's
+// LANES lanes per (row, query head): O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the row's
 // partials in the order of their keys, LSE = ln 2 (M + log2 of that sum). A row that sees no key
 // gets O = 0 and LSE = -inf. Rows that their CTA wrote itself are left alone. What the row needs
 // of the batch is read before the wait for the attention kernel (which had waited for whatever
 // wrote it), the partials after it.
-template <int D>
-struct Partial {
-  float m, l, o[D / 32];
-};
-template <int D>
-__device__ __forceinline__ Partial<D> load_partial(const PagedParams& p, long long slot, int lane) {
-  Partial<D> x;
-  const float2 ml = __ldcg(p.part_ml + slot);
-  x.m = ml.x;
-  x.l = ml.y;
-  if constexpr (D == 64) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + slot * D) + lane);
-    x.o[0] = v.x;
-    x.o[1] = v.y;
-  } else {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * D) + lane);
-    x.o[0] = v.x;
-    x.o[1] = v.y;
-    x.o[2] = v.z;
-    x.o[3] = v.w;
-  }
-  return x;
-}
-
 // x / y in 32 bits where they hold both.
 __device__ __forceinline__ int quotient(long long x, long long y) {
   if (x >> 32 == 0) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(min(y, 0xffffffffLL)));
   return static_cast<int>(x / y);
 }
 
-template <typename T, int D>
+template <typename T, int D, int LANES>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x, hq = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int b = hq < p.Hq ? find_sequence(p.row_start, p.B, row) : -1;
+  constexpr int kPer = D / LANES;                      // dims of a lane, as vectors of kVec
+  constexpr int kVec = kPer < 4 ? kPer : 4;
+  const int lane = threadIdx.x % LANES;
+  const int row = blockIdx.x, hq = (blockIdx.y * 128 + threadIdx.x) / LANES;
+  const int b = find_sequence(p.row_start, p.B, row);
   const int h = hq / p.G, g = hq % p.G;
   const int parts = parts_of(p);
   // per part: units of the item, its first unit (without the sequence's), and the row's place
-  int nk[2] = {0, 0}, at[2], tile[2];
-  long long first[2];
-  bool split[2], whole = false;
+  int nk0 = 0, nk1 = 0, at0 = 0, at1 = 0, tile0 = 0, tile1 = 0;
+  long long first0 = 0, first1 = 0;
+  bool split0 = false, split1 = false, whole = false;
+  auto look = [&](int s, int& nk, int& at, int& tile, long long& first, bool& split) {
+    const SeqView v = seq_view(p, s);
+    const int t = row - v.r0;
+    if (t < 0 || t >= v.n) return;
+    const int item = t / p.item_tokens, in = t - item * p.item_tokens;
+    nk = item_units(p, s, v, item);
+    first = h * head_units(p, s, v) + units_before(p, s, v, item);
+    split = p.streams == 2 && v.n - item * p.item_tokens <= p.tile_tokens;
+    tile = in / p.tile_tokens;
+    at = (in - tile * p.tile_tokens) * p.G + g;
+    whole = writes_rows(p, v, item);
+  };
   if (b >= 0) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= parts) break;
-      const int s = parts == 2 && k == 0 ? -1 : b;
-      const SeqView v = seq_view(p, s);
-      const int t = row - v.r0;
-      const int item = t / p.item_tokens, in = t - item * p.item_tokens;
-      if (t < 0 || t >= v.n) continue;
-      nk[k] = item_units(p, s, v, item);
-      first[k] = h * head_units(p, s, v) + units_before(p, s, v, item);
-      split[k] = p.streams == 2 && v.n - item * p.item_tokens <= p.tile_tokens;
-      tile[k] = in / p.tile_tokens;
-      at[k] = (in - tile[k] * p.tile_tokens) * p.G + g;
-      whole = writes_rows(p, v, item);
-    }
+    if (parts == 2) look(-1, nk0, at0, tile0, first0, split0);
+    look(b, nk1, at1, tile1, first1, split1);
   }
   griddep_wait();
   griddep_launch_dependents();
   if (b < 0) return;                                   // behind the last sequence: left as it was
   const long long U = __ldcg(p.plan), own = __ldcg(p.plan + 1 + b);
+  // the partials in the order of their keys: per part its CTAs' pieces, per piece its streams
+  int c0 = 0, c1 = 0, n0 = 0, n1 = 0;
+  bool mine = hq < p.Hq;
+  if (nk0 > 0) {
+    c0 = quotient(first0, U);
+    n0 = (quotient(first0 + nk0 - 1, U) - c0 + 1) * (split0 ? 2 : 1);
+  }
+  if (nk1 > 0) {
+    const long long u0 = own + first1;
+    c1 = quotient(u0, U);
+    const int pieces = quotient(u0 + nk1 - 1, U) - c1 + 1;
+    if (pieces == 1 && whole) mine = false;            // written by its CTA
+    n1 = pieces * (split1 ? 2 : 1);
+  }
+  const int total = mine ? n0 + n1 : 0;
+  auto slot_of = [&](int i) {
+    const bool k = i >= n0;
+    const bool split = k ? split1 : split0;
+    const int j = k ? i - n0 : i;
+    const int piece = split ? j >> 1 : j, stream = split ? j & 1 : 0;
+    if (piece == 0) return row_slot(p, k ? b : -1, stream, row, hq);
+    return cta_slot(p, (k ? c1 : c0) + piece,
+                    (split ? stream : k ? tile1 : tile0) * (p.slot_rows / p.streams) + (k ? at1 : at0));
+  };
   float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  auto add = [&](const Partial<D>& x) {
-    if (x.l == 0.f) return;                            // saw none of its keys
-    const float m = fmaxf(M, x.m);
-    const float f0 = exp2f(M - m), f1 = exp2f(x.m - m);
-    M = m;
-    L = L * f0 + x.l * f1;
+  for (int i0 = 0; __any_sync(0xffffffffu, i0 < total); i0 += LANES) {
+    // a lane for each of LANES partials: their common maximum, their weights
+    const bool there = i0 + lane < total;
+    const long long slot = there ? slot_of(i0 + lane) : 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (there) ml = __ldcg(p.part_ml + slot);
+    if (ml.y == 0.f) ml.x = -INFINITY;                 // saw none of its keys
+    float top = fmaxf(M, ml.x);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f0 + x.o[i] * f1;
-  };
+    for (int d = LANES / 2; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+    const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+    M = top;
+    float l = w * ml.y;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (k >= parts || nk[k] == 0) continue;
-    const int s = parts == 2 && k == 0 ? -1 : b;
-    const long long u0 = first[k] + (s < 0 ? 0 : own);
-    const int c0 = quotient(u0, U), c1 = quotient(u0 + nk[k] - 1, U);
-    if (c0 == c1 && whole) return;                     // written by its CTA
-    for (int c = c0; c <= c1; ++c) {
-      const long long s0 = c == c0 ? row_slot(p, s, 0, row, hq)
-                                   : cta_slot(p, c, (split[k] ? 0 : tile[k]) * (p.slot_rows / p.streams) + at[k]);
-      if (split[k]) {
-        const long long s1 = c == c0 ? row_slot(p, s, 1, row, hq) : cta_slot(p, c, p.slot_rows / p.streams + at[k]);
-        const Partial<D> x = load_partial<D>(p, s0, lane), y = load_partial<D>(p, s1, lane);
-        add(x);
-        add(y);
-      } else {
-        add(load_partial<D>(p, s0, lane));
+    for (int d = LANES / 2; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    L = L * f + l;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] *= f;
+#pragma unroll 4
+    for (int j = 0; j < LANES; ++j) {
+      if (!__any_sync(0xffffffffu, i0 + j < total)) break;
+      const float wj = __shfl_sync(0xffffffffu, w, j, LANES);
+      const float* src = p.part_o + __shfl_sync(0xffffffffu, slot, j, LANES) * D + lane * kVec;
+      if (wj != 0.f) {                                 // a partial that saw no key holds no numbers
+#pragma unroll
+        for (int i = 0; i < kPer; i += kVec) {
+          if constexpr (kVec == 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src + i * LANES));
+            acc[i] = fmaf(wj, x.x, acc[i]);
+            acc[i + 1] = fmaf(wj, x.y, acc[i + 1]);
+          } else {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + i * LANES));
+            acc[i] = fmaf(wj, x.x, acc[i]);
+            acc[i + 1] = fmaf(wj, x.y, acc[i + 1]);
+            acc[i + 2] = fmaf(wj, x.z, acc[i + 2]);
+            acc[i + 3] = fmaf(wj, x.w, acc[i + 3]);
+          }
+        }
       }
     }
   }
+  if (!mine) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  T* out = static_cast<T*>(p.o) + (static_cast<long long>(row) * p.Hq + hq) * D + lane * kPer;
-  if constexpr (sizeof(T) == 2) {
+  T* out = static_cast<T*>(p.o) + (static_cast<long long>(row) * p.Hq + hq) * D + lane * kVec;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2)
-      *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<float2*>(out + i) = make_float2(acc[i] * inv, acc[i + 1] * inv);
+  for (int i = 0; i < kPer; i += 2) {
+    T* at = out + (i / kVec) * kVec * LANES + i % kVec;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+    else *reinterpret_cast<float2*>(at) = make_float2(acc[i] * inv, acc[i + 1] * inv);
   }
   if (p.lse && lane == 0)
     p.lse[static_cast<long long>(row) * p.Hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+template <typename T, int D>
+cudaError_t launch_merge(cudaStream_t s, const PagedParams& p) {
+  // A warp for a row's head takes up to 32 partials at once (a long sequence's few rows); eight
+  // lanes for one where there are many rows, whose partials are few: four times fewer warps to
+  // look everything up.
+  if (static_cast<long long>(p.rows) * p.Hq < kManyHeads)
+    return launch_pdl(paged_merge_kernel<T, D, 32>, dim3(p.rows, (p.Hq + 3) / 4), dim3(128), 0, s, p);
+  return launch_pdl(paged_merge_kernel<T, D, 8>, dim3(p.rows, (p.Hq + 15) / 16), dim3(128), 0, s, p);
+}
 template <typename T>
 cudaError_t launch_merge(cudaStream_t s, const PagedParams& p) {
-  const dim3 grid(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.Hq + 3) / 4));
-  return p.D == 64 ? launch_pdl(paged_merge_kernel<T, 64>, grid, dim3(128), 0, s, p)
-                   : launch_pdl(paged_merge_kernel<T, 128>, grid, dim3(128), 0, s, p);
+  return p.D == 64 ? launch_merge<T, 64>(s, p) : launch_merge<T, 128>(s, p);
 }
 
 // Weights of key blocks whose query tiles were split over CTAs: the run of continuing CTAs of a

@@ -164,7 +164,8 @@ __device__ __forceinline__ void walk_to(const PagedParams& p, Walk& w, int b) {
 
 // Block-wide: the first unit of every sequence, and this CTA's place in them. units_of_head(b,
 // view) gives the units of one head of sequence b. Every thread of the block calls it; s must
-// hold 2 + blockDim.x / 32 long longs. CTA 0 writes the plan.
+// hold kPlanWords + blockDim.x / 32 long longs. CTA 0 writes the plan.
+constexpr int kPlanWords = 4;
 template <typename HeadUnits>
 __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, HeadUnits&& units_of_head) {
   const int nt = blockDim.x, t = threadIdx.x;
@@ -174,9 +175,11 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
   const int per = (n_seq + nt - 1) / nt;
   const int b0 = b_first + min(n_seq, t * per), b1 = b_first + min(n_seq, (t + 1) * per);
   long long mine = 0;
+  SeqView view{};
   for (int b = b0; b < b1; ++b) {
     if (blockIdx.x == 0 && b >= 0) seq_check(p, b);
-    mine += p.Hkv * units_of_head(b, seq_view(p, b));
+    view = seq_view(p, b);
+    mine += p.Hkv * units_of_head(b, view);
   }
   long long incl = mine;
 #pragma unroll
@@ -184,11 +187,11 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
     const long long o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
   }
-  if (lane == 31) s[2 + warp] = incl;
+  if (lane == 31) s[kPlanWords + warp] = incl;
   __syncthreads();
   long long before = 0, total = 0;
   for (int w = 0; w < warps; ++w) {
-    const long long x = s[2 + w];
+    const long long x = s[kPlanWords + w];
     if (w < warp) before += x;
     total += x;
   }
@@ -207,13 +210,17 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
     long long at = before;
     int b = b0;
-    for (;; ++b) {
-      const long long x = p.Hkv * units_of_head(b, seq_view(p, b));
-      if (u0 < at + x) break;
-      at += x;
-    }
+    if (b1 - b0 > 1)                           // else it is the one whose view is at hand
+      for (;; ++b) {
+        view = seq_view(p, b);
+        const long long x = p.Hkv * units_of_head(b, view);
+        if (u0 < at + x) break;
+        at += x;
+      }
     s[0] = at;
     s[1] = b;
+    s[2] = (static_cast<long long>(view.n) << 32) | static_cast<uint32_t>(view.r0);
+    s[3] = view.len;
   }
   __syncthreads();
   Walk w{};
@@ -221,7 +228,7 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
   w.u1 = u1;
   if (u0 < u1) {
     const int b = static_cast<int>(s[1]);
-    w.v = seq_view(p, b);
+    w.v = {static_cast<int>(s[2]), static_cast<int>(s[2] >> 32), static_cast<int>(s[3])};
     walk_to(p, w, b);
     const long long uph = units_of_head(b, w.v);
     w.h = static_cast<int>((u0 - s[0]) / uph);

@@ -72,7 +72,7 @@ struct Bars {
   SegmentRing ring;
   uint32_t tmem;
   int abort;
-  long long plan[2 + kThreads / 32];
+  long long plan[kPlanWords + kThreads / 32];
 };
 
 // Steps of stream w in a segment of `blocks` key blocks.
@@ -118,8 +118,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,6 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bar.tmem, 512);
     tmem_relinquish();
   }
+  griddep_wait();                              // everything above is this CTA's own
+  griddep_launch_dependents();
   Walk walk = plan_walk(p, bar.plan, [&](int b, const SeqView& v) { return head_units(p, b, v); });
   tc_fence_before();
   __syncthreads();

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
   float* ks = qs + ROWS * LD;                  // [kKT][LD]
   float* vs = ks + kKT * LD;                   // [kKT][LD]
   float* ps = vs + kKT * LD;                   // [ROWS][LP]
-  __shared__ long long plan_s[2 + kThreads / 32];
+  __shared__ long long plan_s[kPlanWords + kThreads / 32];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Walk w = plan_walk(p, plan_s, [&](int b, const SeqView& v) { return head_units(p, b, v); });
   walk_to_item(p, w);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   extern __shared__ float sm[];
   float* qs = sm;                              // [ROWS][LD]
   float* ks = qs + ROWS * LD;                  // [kKT][LD]
-  __shared__ long long plan_s[2 + kThreads / 32];
+  __shared__ long long plan_s[kPlanWords + kThreads / 32];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Walk w = plan_walk(p, plan_s, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);

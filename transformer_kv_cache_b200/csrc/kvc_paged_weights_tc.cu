@@ -50,7 +50,7 @@ struct Bars {
   int finite[kQueryStages];                    // 1: every row's log-sum-exp is
   uint32_t tmem;
   int abort;
-  long long plan[2 + kThreads / 32];
+  long long plan[kPlanWords + kThreads / 32];
 };
 
 // Segments in the ring: i = key block, [k0, k1) = query tiles, nk = the sequence's query tiles,
@@ -85,8 +85,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ PagedParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -116,12 +114,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ring_init(bar.ring, 11);                   // every warp but the one that fills it
     bar.abort = 0;
     mbar_fence_init();
-    p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (warp == 1) {
     tmem_alloc(&bar.tmem, 512);
     tmem_relinquish();
   }
+  griddep_wait();                              // everything above is this CTA's own
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk walk = plan_walk(p, bar.plan, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   tc_fence_before();
   __syncthreads();
