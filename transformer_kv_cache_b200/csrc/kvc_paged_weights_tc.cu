@@ -13,13 +13,20 @@
 // runs under this one's exponentials. A sequence whose rows fit one tile keeps it in shared memory
 // from key block to key block.
 //
-// Roles (384 threads): warp 3 walks the schedule and hands out its segments through a ring;
-// warp 0 loads the key tiles by TMA (a page to a copy, looked up one block ahead); warp 2 loads
-// the query tiles and puts their rows' log2-sum-exp and last visible key beside them; warp 1 issues
-// the MMAs (both operands in shared memory); warps 4-7 and 8-11 are the exponentials and sums of
-// stream 0 and 1 (thread = key). A warp whose keys every row of the tile sees, which is all but the
-// last tiles of a causal call, adds without looking at the rows' limits (where a row's log-sum-exp
-// is not finite, nothing is skipped: +inf adds exactly nothing, NaN stays NaN).
+// Roles: warp 3 walks the schedule and hands out its segments through a ring; warp 0 loads the key
+// tiles by TMA (a page to a copy, looked up one block ahead); warp 2 loads the query tiles and puts
+// their rows' log2-sum-exp and last visible key beside them; warp 1 issues the
+// MMAs (both operands in shared memory); warps 4 and up are the exponentials and sums (thread =
+// key). A warp whose keys every row of the tile sees, which is all but the last tiles of a causal
+// call, adds without looking at the rows' limits (where a row's log2-sum-exp is not finite, nothing
+// is skipped: +inf adds exactly nothing, NaN stays NaN).
+//
+// Two forms. Where the sequences' rows do not fill a query tile, on average (decode steps), the keys'
+// bytes are the bound: 4 sum warps a stream, most of the shared memory for key tiles (20 warps took 92 for
+// 84 us at 32 sequences of 8,192 tokens). Else the exponentials are: 8 sum warps a stream, four for
+// a query tile's first 64 rows and four for the others (the halves of a key's sum meet in shared
+// memory at the end of a block), so that four warps a scheduler cover one another's waits, an
+// issuing warp for each stream, and as much room for query tiles as for key tiles.
 #include "kvc_paged.cuh"
 #include "kvc_paged_math.cuh"
 
@@ -28,29 +35,33 @@ namespace {
 
 using namespace paged;
 
-constexpr int kThreads = 384;
 constexpr int kTile = 128;                     // keys of a stream, query rows of a tile
-constexpr int kQueryStages = 2;
 constexpr int kPoly8 = 3;                      // of 8 pairs, the exponentials on the FMA pipe
 
-template <int D>
+template <int D, bool kMany>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kKeyStages = D == 128 ? 4 : 8;      // key tiles (two to a block)
-  static constexpr int kSmem = 1024 + (kKeyStages + kQueryStages) * kTileBytes + kQueryStages * kTile * 8 + 1152;
+  static constexpr int kKeyStages = (kMany ? 3 : 4) * (D == 128 ? 1 : 2);    // key tiles (two to a block)
+  static constexpr int kQueryStages = kMany ? 3 * (D == 128 ? 1 : 2) : 2;
+  static constexpr int kSumWarps = kMany ? 16 : 8;
+  static constexpr int kIssuers = kMany ? 2 : 1;           // warp 1, and the last one
+  static constexpr int kThreads = 32 * (4 + kSumWarps + kIssuers - 1);
+  static constexpr int kSmem =
+      1024 + (kKeyStages + kQueryStages) * kTileBytes + kQueryStages * kTile * 8 + 2 * kTile * 4 + 1408;
 };
 
 struct Bars {
   uint64_t k_full[8], k_empty[8];
-  uint64_t q_full[kQueryStages], q_empty[kQueryStages];
+  uint64_t q_full[6], q_empty[6];
   uint64_t s_full[2][2], s_empty[2][2];        // [stream][buffer]
-  uint64_t drained;
+  uint64_t x_full[2], x_empty[2];              // a stream's second half sums
+  uint64_t drained[2];
   SegmentRing ring;
-  int finite[kQueryStages];                    // 1: every row's log-sum-exp is
+  int finite[6];                               // 1: every row's log-sum-exp is
   uint32_t tmem;
   int abort;
-  long long plan[kPlanWords + kThreads / 32];
+  long long plan[kPlanWords + 24];
 };
 
 // Segments in the ring: i = key block, [k0, k1) = query tiles, nk = the sequence's query tiles,
@@ -81,37 +92,43 @@ __device__ __forceinline__ void add_all(const uint32_t (&s)[32], const float* y,
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kMany>
+__global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ PagedParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kMany>;
+  constexpr int kQueryStages = C::kQueryStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* k_s = smem;                                     // [stage][8 keys][half][key][128 B]
   uint8_t* q_s = k_s + C::kKeyStages * C::kTileBytes;      // [stage][half][128 rows][128 B]
   float* lse_s = reinterpret_cast<float*>(q_s + kQueryStages * C::kTileBytes);   // [stage][128] -lse2
   int* limit_s = reinterpret_cast<int*>(lse_s + kQueryStages * kTile);           // [stage][128] keys that the row sees
-  Bars& bar = *reinterpret_cast<Bars*>(limit_s + kQueryStages * kTile);
-  static_assert(sizeof(Bars) <= 1152, "barriers");
+  float* half_s = reinterpret_cast<float*>(limit_s + kQueryStages * kTile);      // [stream][128] sums of the second rows
+  Bars& bar = *reinterpret_cast<Bars*>(half_s + 2 * kTile);
+  static_assert(sizeof(Bars) <= 1408, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bar.abort;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kKeyStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.k_empty[i], 1);           // the stream's issuer
     }
     for (int i = 0; i < kQueryStages; ++i) {
       mbar_init(&bar.q_full[i], 2);            // the bytes, and the rows' statistics
-      mbar_init(&bar.q_empty[i], 9);           // the products, and the 8 warps that read the statistics
+      mbar_init(&bar.q_empty[i], C::kIssuers + C::kSumWarps);   // the products, and who reads the statistics
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.s_full[i >> 1][i & 1], 1);
-      mbar_init(&bar.s_empty[i >> 1][i & 1], 4);
+      mbar_init(&bar.s_empty[i >> 1][i & 1], C::kSumWarps / 2);
     }
-    mbar_init(&bar.drained, 1);
-    ring_init(bar.ring, 11);                   // every warp but the one that fills it
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.x_full[i], 4);
+      mbar_init(&bar.x_empty[i], 4);
+      mbar_init(&bar.drained[i], 1);
+    }
+    ring_init(bar.ring, C::kThreads / 32 - 1); // every warp but the one that fills it
     bar.abort = 0;
     mbar_fence_init();
   }
@@ -206,50 +223,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------------ queries and their statistics
     if (lane == 0) tma_prefetch_desc(&tmap_q);
-    int eq = 0;
-    bool ok = true;
-    for (int sg = 0; ok; ++sg) {
-      Segment g;
-      ok = ring_take(bar.ring, sg, g, abort, p.err);
-      if (!ok || g.nk == 0) break;
-      if (!g.two) continue;
-      for (int t = g.k0; t < g.k1 && ok; ++t, ++eq) {
-        const int st = eq % kQueryStages;
-        const int tok0 = t * p.tile_tokens, rows = tile_rows(p, g, t);
-        float y[4];                            // loaded before the wait for the stage
+    int tok[4], head[4];                       // this lane's rows of any tile
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 32 * i + lane;
-          y[i] = 0.f;
-          if (r < rows)
-            y[i] = __ldg(p.lse + static_cast<long long>(g.v.r0 + tok0 + r / p.G) * p.Hq + g.h * p.G + r % p.G);
-        }
-        ok = eq < kQueryStages || mbar_wait_bounded(&bar.q_empty[st], ((eq / kQueryStages) - 1) & 1, abort, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar.q_full[st], C::kHalves * p.tile_tokens * p.G * 128);
-          for (int c = 0; c < C::kHalves; ++c)
-            tma_load_3d(q_s + st * C::kTileBytes + c * (kTile * 128), &tmap_q, &bar.q_full[st], c * 64, g.h * p.G,
-                        g.v.r0 + tok0);
-        }
-        const bool fin = __all_sync(0xffffffffu, isfinite(y[0]) && isfinite(y[1]) && isfinite(y[2]) && isfinite(y[3]));
-        if (lane == 0) bar.finite[st] = fin;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 32 * i + lane;
-          lse_s[st * kTile + r] = -1.4426950408889634f * y[i];
-          limit_s[st * kTile + r] = r < rows ? key_limit(p, g.b, g.v, tok0 + r / p.G) : 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.q_full[st]);
+    for (int i = 0; i < 4; ++i) {
+      tok[i] = (32 * i + lane) / p.G;
+      head[i] = (32 * i + lane) % p.G;
+    }
+    int eq = 0, sg = 0, t = 0;
+    Segment g{};
+    // to the next tile that is to be loaded; its rows' log-sum-exp arrives while a stage is waited for
+    float next[4];
+    auto advance = [&](bool first) {
+      ++t;
+      while (first || t >= g.k1) {
+        first = false;
+        if (!ring_take(bar.ring, sg++, g, abort, p.err) || g.nk == 0) return false;
+        t = g.two ? g.k0 : g.k1;               // else the tile is there already
       }
+      const int rows = tile_rows(p, g, t);
+      const float* lse = p.lse + static_cast<long long>(g.v.r0 + t * p.tile_tokens) * p.Hq + g.h * p.G;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) next[i] = 32 * i + lane < rows ? __ldg(lse + static_cast<long long>(tok[i]) * p.Hq + head[i]) : 0.f;
+      return true;
+    };
+    bool more = advance(true);
+    while (more) {
+      const int st = eq % kQueryStages;
+      const int tok0 = t * p.tile_tokens, rows = tile_rows(p, g, t);
+      bool ok = eq < kQueryStages || mbar_wait_bounded(&bar.q_empty[st], ((eq / kQueryStages) - 1) & 1, abort, p.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.q_full[st], C::kHalves * p.tile_tokens * p.G * 128);
+        for (int c = 0; c < C::kHalves; ++c)
+          tma_load_3d(q_s + st * C::kTileBytes + c * (kTile * 128), &tmap_q, &bar.q_full[st], c * 64, g.h * p.G,
+                      g.v.r0 + tok0);
+      }
+      const bool fin =
+          __all_sync(0xffffffffu, isfinite(next[0]) && isfinite(next[1]) && isfinite(next[2]) && isfinite(next[3]));
+      if (lane == 0) bar.finite[st] = fin;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + lane;
+        lse_s[st * kTile + r] = -1.4426950408889634f * next[i];
+        limit_s[st * kTile + r] = r < rows ? key_limit(p, g.b, g.v, tok0 + tok[i]) : 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_full[st]);
+      ++eq;
+      // only now: the next tile may lie many segments on, which wait for this one
+      more = advance(false);
     }
     if (lane == 0)
       for (int i = max(0, eq - kQueryStages); i < eq; ++i)
         mbar_wait_drain(&bar.q_full[i % kQueryStages], (i / kQueryStages) & 1, p.err);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ products
+  } else if (warp == 1 || warp == 4 + C::kSumWarps) {
+    // ------------------------------------------------------------------ products of streams [w0, w1)
+    const int w0 = warp == 1 ? 0 : 1, w1 = C::kIssuers == 1 ? 2 : w0 + 1;
     const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
     const uint64_t k_desc = sw128_desc(smem_u32(k_s), 16, C::kHalves * 1024);
     const bool leader = elect_one();
@@ -276,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = q.eq % kQueryStages;
         const int cols = (tile_rows(p, g, t) + 15) & ~15;
         const uint32_t idesc = idesc_f16kind(1, kTile, 16, 0, 0) + ((static_cast<uint32_t>(cols - 16) >> 3) << 17);
-        for (int w = 0; w < nt; ++w) {
+        ok = __all_sync(0xffffffffu, r);
+        for (int w = w0; w < min(nt, w1) && ok; ++w) {
           const int ks = (ek + w) % C::kKeyStages, x = steps[w] & 1;
           if (t == g.k0) r = r && mbar_wait_bounded(&bar.k_full[ks], ((ek + w) / C::kKeyStages) & 1, abort, p.err);
           if (steps[w] >= 2) r = r && mbar_wait_bounded(&bar.s_empty[w][x], ((steps[w] >> 1) - 1) & 1, abort, p.err);
@@ -306,16 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ek += nt;
     }
-    if (leader) mma_commit(&bar.drained);
+    if (leader) mma_commit(&bar.drained[w0]);
     __syncwarp();
-    mbar_wait_drain(&bar.drained, 0, p.err);
+    mbar_wait_drain(&bar.drained[w0], 0, p.err);
   } else {
-    // ------------------------------------------------------------------ sums of stream w
-    const int w = (warp - 4) >> 2, wq = warp & 3;
+    // ------------------------------------------------------------------ sums of stream w (rows 64 half ..)
+    const int w = kMany ? (warp - 4) >> 3 : (warp - 4) >> 2, half = kMany ? ((warp - 4) >> 2) & 1 : 0, wq = warp & 3;
     const uint32_t s_col = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 2 * w * 128;
     const float c = p.scale_log2;
     const uint64_t c2 = pk2(c, c);
-    int steps = 0;
+    int steps = 0, met = 0;                    // products, and blocks whose halves met
     QueryWalk q;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int st = q.eq % kQueryStages;
         if (mine) {
-          const int rows = tile_rows(p, g, t);
+          const int rows = min(tile_rows(p, g, t), kMany ? 64 * half + 64 : kTile);
           const int x = steps & 1;
           ok = ok && mbar_wait_bounded(&bar.s_full[w][x], (steps >> 1) & 1, abort, p.err);
           ok = __all_sync(0xffffffffu, ok);
@@ -350,30 +380,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool all = bar.finite[st] && min(key0 + 31, g.v.len - 1) < limit[0];
           float rest = 0.f;
           uint64_t sum0 = 0, sum1 = 0;
-          int done = 0;
-          if (all && rows >= 32) {
-            uint32_t a[32], b[32];             // the next columns arrive under these ones' exponentials
-            tmem_ld32(buf, a);
-            tmem_ld_wait();
-            for (;; done += 64) {
-              const bool second = done + 64 <= rows;
-              if (second) tmem_ld32(buf + done + 32, b);
-              add_all(a, y + done, c2, sum0, sum1);
-              if (!second) {
-                done += 32;
-                break;
-              }
+          int done = 64 * half;
+          if (all)
+            for (; done + 32 <= rows; done += 32) {
+              uint32_t s[32];
+              tmem_ld32(buf + done, s);
               tmem_ld_wait();
-              const bool third = done + 96 <= rows;
-              if (third) tmem_ld32(buf + done + 64, a);
-              add_all(b, y + done + 32, c2, sum0, sum1);
-              if (!third) {
-                done += 64;
-                break;
-              }
-              tmem_ld_wait();
+              add_all(s, y + done, c2, sum0, sum1);
             }
-          }
           for (; done < rows; done += 16) {
             uint32_t s[16];
             tmem_ld16(buf + done, s);
@@ -399,8 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      const int at = w * kTile + wq * 32 + lane;
+      if (kMany && (g.nk > 1 || tile_rows(p, g, 0) > 64)) {
+        // the second rows' sum to the first ones' warp of the same keys
+        if (half == 1) {
+          ok = met == 0 || mbar_wait_bounded(&bar.x_empty[w], (met - 1) & 1, abort, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          half_s[at] = total;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.x_full[w]);
+        } else {
+          ok = mbar_wait_bounded(&bar.x_full[w], met & 1, abort, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          total += half_s[at];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.x_empty[w]);
+        }
+        ++met;
+      }
+      if (half == 1) continue;
       if (g.k0 > 0) {
-        p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + w * kTile + wq * 32 + lane] = total;
+        p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + at] = total;
         if (warp == 4 && lane == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.i, 1);
       } else if (key < g.v.len) {
         p.scores[(static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key] += total;
@@ -415,16 +450,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kMany>
 cudaError_t launch(cudaStream_t s, const PagedParams& p, const CUtensorMap& q, const CUtensorMap& k) {
+  using C = Cfg<D, kMany>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_tc_kernel<D>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_tc_kernel<D, kMany>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   return e != cudaSuccess
              ? e
-             : launch_pdl(paged_weights_tc_kernel<D>, dim3(p.grid), dim3(kThreads), Cfg<D>::kSmem, s, q, k, p);
+             : launch_pdl(paged_weights_tc_kernel<D, kMany>, dim3(p.grid), dim3(C::kThreads), C::kSmem, s, q, k, p);
 }
 
 }  // namespace
@@ -432,7 +468,10 @@ cudaError_t launch(cudaStream_t s, const PagedParams& p, const CUtensorMap& q, c
 cudaError_t launch_paged_weights_tc(cudaStream_t s, const PagedParams& p) {
   CUtensorMap q, k;
   if (!encode_rows_tmap(&q, p.q, p) || !encode_slots_tmap(&k, p.k_pool, p)) return cudaErrorInvalidValue;
-  return p.D == 64 ? launch<64>(s, p, q, k) : launch<128>(s, p, q, k);
+  // a sequence's rows fill more than one tile, on average
+  const bool many = p.rows > static_cast<long long>(p.B) * p.tile_tokens;
+  if (p.D == 64) return many ? launch<64, true>(s, p, q, k) : launch<64, false>(s, p, q, k);
+  return many ? launch<128, true>(s, p, q, k) : launch<128, false>(s, p, q, k);
 }
 
 }  // namespace kvc
