@@ -7,29 +7,27 @@
 //
 // An item is up to two tiles of 128 packed query rows (tokens x the G query heads of one KV
 // head, whole tokens only) that share the K and V tiles in shared memory. The CTA runs two
-// streams, each with score buffers S in TMEM (128 rows x kStep keys fp32, overwritten by their
-// own weights P as bf16), an accumulator O (128 x D fp32) and a softmax
-// warpgroup, so that one stream's products run under the other's exponentials. With two tiles a
-// stream is a tile; an item of one tile (a decode step's few rows) gives its key blocks to the
-// streams by turns, each with a maximum and sum of its own.
+// streams, each with a score tile S in TMEM (128 rows x 128 keys fp32, overwritten by its own
+// weights P as bf16), so that one stream's products run under the other's exponentials. With
+// two tiles a stream is a tile; an item of one tile (a decode step's few rows) gives its key tiles
+// to the streams by turns, each with a maximum and sum of its own.
 //
-// TMEM decides the step: with D = 64 a stream has two S buffers of 64 keys, and the issuer keeps
-// S one step ahead of the softmax; with D = 128 the accumulators leave one S buffer of 128 keys
-// (a product of 64 keys would read the query operand from shared memory faster than that can
-// give it: 48 cycles for 32 of the tensor core).
+// With D = 64 the exponentials are the bound and TMEM has room: a stream's keys are halved, 64 of a
+// tile to each of two softmax warpgroups with an accumulator O, maximum and sum of their own,
+// which are joined through shared memory at the end of a segment. Four warps a scheduler then
+// cover one another's waits (two, with S double-buffered instead: 586 TFLOP/s over 73,292 keys).
+// With D = 128 the two accumulators fill TMEM, and a softmax warpgroup takes all 128 keys.
 //
-// Roles (384 threads): warp 3 walks the schedule and hands out its segments through a ring in
-// shared memory, some segments ahead (the walk's loads and divisions are off everybody else's
-// path), and loads the queries by TMA as a 3-D box (dims, heads, tokens), which packs the rows of
-// any group size; warp 0 loads K and V by TMA (a page's slots, all dims, to a box: its rows go by
-// eights, the 64-dim halves of eight rows after one another, so that one copy serves a page and
-// rows keep one distance; one ring in the order K0 V0 K1 V1 ..., the next tile's pages looked up
-// one tile ahead, across segments); warp 1 issues the
-// MMAs (S = Q K^T: both operands in shared memory; O += P V: P in TMEM, V as an MN-major
-// operand); with D = 128 it takes the streams by turns, which
-// keeps one stream's products under the other's softmax; with D = 64, where a product is so short
-// that issuing it is what takes the time, warp 2 issues stream 1's; warps 4-7 and 8-11 are the
-// softmax of stream 0 and 1 (thread = row = TMEM lane).
+// Roles: warp 3 walks the schedule and hands out its segments through a ring in shared memory,
+// some segments ahead (the walk's loads and divisions are off everybody else's path), and loads the
+// queries by TMA as a 3-D box (dims, heads, tokens), which packs the rows of any group size; warp 0
+// loads K and V by TMA (a page's slots, all dims, to a box: its rows go by eights, the 64-dim
+// halves of eight rows after one another, so that one copy serves a page and rows keep one
+// distance; one ring in the order K0 V0 K1 V1 ..., the next tile's pages looked up one tile ahead,
+// across segments); warp 1 issues the MMAs (S = Q K^T: both operands in shared memory; O += P V:
+// P in TMEM, V as an MN-major operand), the streams by turns, which keeps one stream's products
+// under the other's softmax (a warp for each let them run in step: 771 for 952 TFLOP/s at D =
+// 128); the warps from 4 on are the softmax (thread = row = TMEM lane).
 //
 // Slots past a sequence's length are never used: boxes past it are loaded from behind the
 // pool's end, which TMA fills with zeros, the last box of V is copied by the loading warp's threads
@@ -45,38 +43,41 @@ namespace {
 
 using namespace paged;
 
-constexpr int kThreads = 384;
 constexpr int kTile = 128;                     // query rows of a tile, keys of a unit
 constexpr float kGrow = 8.0f;                  // a weight above 2^8 moves the row's reference maximum
-constexpr int kRegsLow = 88, kRegsHigh = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the registers at launch
 constexpr int kAhead = 3;                      // segments handed out before their queries are loaded
 
-template <int D>
+template <int D, int SUB>
 struct Cfg {
   static constexpr int kHalves = D / 64;                       // 128-byte swizzled blocks of a row
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kStep = D == 128 ? 128 : 64;            // keys of a step of a stream
-  static constexpr int kBufs = D == 128 ? 1 : 2;               // score buffers of a stream
-  static constexpr int kPerTile = kTile / kStep;               // steps of a key tile
-  static constexpr int kIssuers = D == 128 ? 1 : 2;            // warps that issue the products
-  static constexpr int kPoly8 = D == 128 ? 0 : 2;              // of 8 pairs, the exponentials on the FMA pipe
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + 1152;
+  static constexpr int kStages = D == 128 ? 5 : SUB == 1 ? 10 : 7;
+  static constexpr int kSub = SUB;                             // softmax warpgroups of a stream
+  static constexpr int kCols = kTile / kSub;                   // keys of a tile for each
+  static constexpr int kSoftWarps = 8 * kSub;
+  static constexpr int kThreads = 128 + 32 * kSoftWarps;
+  // registers of warps 0 to 3 and of the softmax warps: in all those at launch, 168 or 96 a thread
+  static constexpr int kRegsLow = SUB == 1 ? 88 : 64, kRegsHigh = SUB == 1 ? 208 : 104;
+  static constexpr int kPoly8 = SUB == 1 ? 0 : 2;              // of 8 pairs, the exponentials on the FMA pipe
+  static constexpr int kJoinBytes = kSub == 2 ? 2 * kTile * (D * 4 + 8) : 0;
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kJoinBytes + 1152;
 };
 
 struct Bars {
   uint64_t full[10], empty[10];                // K and V tiles
   uint64_t q_full[2], q_empty[2];              // query slots
-  uint64_t s_full[2][2], p_full[2][2];         // [stream][buffer]
-  uint64_t pv_done[2], o_full[2], o_free[2], drained[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t x_full[2], x_empty[2];              // the second warpgroup's results in shared memory
+  uint64_t drained;
   SegmentRing ring;
   uint32_t tmem;
   int abort;
-  long long plan[kPlanWords + kThreads / 32];
+  long long plan[kPlanWords + 20];
 };
 
-// Steps of stream w in a segment of `blocks` key blocks.
-__device__ __forceinline__ int stream_steps(bool two, int w, int blocks) { return two ? blocks : (blocks - w + 1) >> 1; }
+// Steps of stream w in a segment of n key tiles.
+__device__ __forceinline__ int stream_steps(bool two, int w, int n) { return two ? n : (n - w + 1) >> 1; }
 
 // Weights of one row's step: P = 2^(s c - m) as bf16 pairs, returning their sum (before the
 // rounding). kPoly of every 8 pairs go to the FMA pipe, the others to the MUFU, spread through the
@@ -114,16 +115,18 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {
   return max3_nan(max3_nan(a[0], a[1], a[2]), max3_nan(a[3], a[4], a[5]), max_nan(a[6], a[7]));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int SUB>
+__global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, SUB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                     // [slot][half][128 rows][128 B]
   uint8_t* kv_s = q_s + 2 * C::kTileBytes;                 // [stage][8 keys][half][key][128 B]
-  Bars& bar = *reinterpret_cast<Bars*>(kv_s + C::kStages * C::kTileBytes);
+  float4* join_o = reinterpret_cast<float4*>(kv_s + C::kStages * C::kTileBytes);    // [stream][4 dims][128 rows]
+  float2* join_ml = reinterpret_cast<float2*>(join_o + (C::kSub == 2 ? 2 * kTile * D / 4 : 0));   // [stream][128 rows]
+  Bars& bar = *reinterpret_cast<Bars*>(join_ml + (C::kSub == 2 ? 2 * kTile : 0));
   static_assert(sizeof(Bars) <= 1152, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bar.abort;
@@ -131,21 +134,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], C::kIssuers);
+      mbar_init(&bar.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
-      mbar_init(&bar.q_empty[i], C::kIssuers);
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&bar.s_full[i][x], 1);
-        mbar_init(&bar.p_full[i][x], 4);
-      }
-      mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&bar.q_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4 * C::kSub);
       mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.o_free[i], 4);
-      mbar_init(&bar.drained[i], 1);
+      mbar_init(&bar.o_free[i], 4 * C::kSub);
+      mbar_init(&bar.x_full[i], 4);
+      mbar_init(&bar.x_empty[i], 4);
     }
-    ring_init(bar.ring, 9 + C::kIssuers);      // everybody but warp 3 and an idle warp 2
+    mbar_init(&bar.drained, 1);
+    ring_init(bar.ring, 2 + C::kSoftWarps);    // warps 0, 1 and the softmax
     bar.abort = 0;
     mbar_fence_init();
   }
@@ -160,11 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  // TMEM columns: S buffer x of stream w at w * 128 + x * kStep, O of stream w at 256 + w * D
+  // TMEM columns: S of stream w at 128 w, the weights of its warpgroup j at 128 w + 64 j, their O at
+  // 256 + (w * kSub + j) * D
   const int blk = min(1 << p.page_shift, kTile);           // slots of a box
 
   if (warp == 0) {
-    reg_dealloc<kRegsLow>();
+    reg_dealloc<C::kRegsLow>();
     // ------------------------------------------------------------------ K and V
     if (lane == 0) {
       tma_prefetch_desc(&tmap_k);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, e - C::kStages); i < e; ++i)
         mbar_wait_drain(&bar.full[i % C::kStages], (i / C::kStages) & 1, p.err);
   } else if (warp == 3) {
-    reg_dealloc<kRegsLow>();
+    reg_dealloc<C::kRegsLow>();
     // ------------------------------------------------------------------ schedule and queries
     if (lane == 0) {
       tma_prefetch_desc(&tmap_q);
@@ -286,159 +289,167 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i)
         if (used[i]) mbar_wait_drain(&bar.q_full[i], (used[i] - 1) & 1, p.err);
     }
-  } else if (warp < 3) {
-    reg_dealloc<kRegsLow>();
-    // ------------------------------------------------------------------ products of streams [w0, w1)
-    const int w0 = C::kIssuers == 2 ? warp - 1 : 0, w1 = C::kIssuers == 2 ? w0 + 1 : 2;
-    if (warp <= C::kIssuers) {
-      const bool leader = elect_one();         // the warp waits, one lane issues
-      const uint32_t idesc_s = idesc_f16kind(1, kTile, C::kStep, 0, 0);
-      const uint32_t idesc_o = idesc_f16kind(1, kTile, D, 0, 1);
-      // addresses stay below 2^18: an offset adds to the descriptor's address field
-      const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
-      const uint64_t k_desc = sw128_desc(smem_u32(kv_s), 16, C::kHalves * 1024);
-      const uint64_t v_desc = sw128_desc(smem_u32(kv_s), 1024, C::kHalves * 1024);
-      int e0 = 0, slot = 0, used[2] = {0, 0};  // first ring entry of the segment, next query slot
-      int uu[2] = {0, 0}, segs[2] = {0, 0};    // steps and segments of each stream
-      bool ok = true;
-      for (int sg = 0;; ++sg) {
-        Segment g;
-        ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
-        if (!ok || g.nk == 0) break;
-        const bool two = g.two;
-        const int blocks = (g.k1 - g.k0) * C::kPerTile;
-        const int steps[2] = {stream_steps(two, 0, blocks), stream_steps(two, 1, blocks)};
-        const int qs[2] = {slot, two ? slot ^ 1 : slot};
-        for (int w = w0; w < w1 && (w == w0 || two); ++w)
-          ok = ok && mbar_wait_bounded(&bar.q_full[qs[w]], used[qs[w]] & 1, abort, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        ++used[slot];
-        if (two) ++used[slot ^ 1];
-        else slot ^= 1;
-        // Stream w's step u takes key block two ? u : 2 u + w. One issuer takes the streams by turns,
-        // so the later one's product frees a tile; of two issuers each has a vote.
-        auto issue_s = [&](int w, int u) {
-          const int bk = two ? u : 2 * u + w, hb = bk % C::kPerTile;
-          const int e = e0 + 2 * (bk / C::kPerTile), st = e % C::kStages;
-          if (!two || (hb == 0 && w == w0)) {  // else waited for already
-            const bool r = mbar_wait_bounded(&bar.full[st], (e / C::kStages) & 1, abort, p.err);
-            if (!__all_sync(0xffffffffu, r)) return false;
-          }
-          tc_fence_after();
-          const int x = (uu[w] + u) % C::kBufs;
-          const uint64_t qd = q_desc + (qs[w] * C::kTileBytes >> 4);
-          const uint64_t kd = k_desc + (st * C::kTileBytes + hb * (C::kStep * D * 2) >> 4);
-          if (leader) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              const uint32_t qo = ((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4;
-              const uint32_t ko = ((c >> 2) * 1024 + (c & 3) * 32) >> 4;
-              mma_ss(tmem + w * 128 + x * C::kStep, qd + qo, kd + ko, idesc_s, c > 0 ? 1u : 0u);
-            }
-            mma_commit(&bar.s_full[w][x]);
-            const bool last = two ? u + 1 == steps[w] : C::kIssuers == 2 ? u + 1 == steps[w] : bk + 1 == blocks;
-            if (C::kIssuers == 2 ? !two || hb == C::kPerTile - 1 : hb == C::kPerTile - 1 && (w == 1 || !two))
-              mma_commit(&bar.empty[st]);
-            if (last) {                          // the last product that reads these queries
-              mma_commit(&bar.q_empty[qs[w]]);
-              if (C::kIssuers == 2 && two) mma_commit(&bar.q_empty[qs[w]]);
-            }
-          }
-          __syncwarp();
-          return true;
-        };
-        auto issue_pv = [&](int w, int u) {
-          const int bk = two ? u : 2 * u + w, hb = bk % C::kPerTile;
-          const int e = e0 + 2 * (bk / C::kPerTile) + 1, st = e % C::kStages;
-          const int x = (uu[w] + u) % C::kBufs;
-          bool r = true;
-          if (!two || (hb == 0 && w == w0)) r = mbar_wait_bounded(&bar.full[st], (e / C::kStages) & 1, abort, p.err);
-          if (u == 0 && segs[w] > 0) r = r && mbar_wait_bounded(&bar.o_free[w], (segs[w] - 1) & 1, abort, p.err);
-          r = r && mbar_wait_bounded(&bar.p_full[w][x], ((uu[w] + u) / C::kBufs) & 1, abort, p.err);
-          if (!__all_sync(0xffffffffu, r)) return false;
-          tc_fence_after();
-          const uint64_t vd = v_desc + (st * C::kTileBytes + hb * (C::kStep * D * 2) >> 4);
-          if (leader) {
-#pragma unroll
-            for (int c = 0; c < C::kStep / 16; ++c)
-              mma_ts(tmem + 256 + w * D, tmem + w * 128 + x * C::kStep + c * 8, vd + c * (D * 32 >> 4), idesc_o,
-                     u > 0 || c > 0 ? 1u : 0u);
-            if (C::kBufs > 1) mma_commit(&bar.pv_done[w]);
-            if (u + 1 == steps[w]) mma_commit(&bar.o_full[w]);
-          }
-          __syncwarp();
-          return true;
-        };
-        auto release_v = [&](int w, int u) {
-          const int bk = two ? u : 2 * u + w, hb = bk % C::kPerTile;
-          if (leader && (C::kIssuers == 2 ? !two || hb == C::kPerTile - 1 : hb == C::kPerTile - 1 && (w == 1 || !two)))
-            mma_commit(&bar.empty[(e0 + 2 * (bk / C::kPerTile) + 1) % C::kStages]);
-          __syncwarp();
-        };
-        for (int u = 0; u < C::kBufs && ok; ++u)
-          for (int w = w0; w < w1 && ok; ++w)
-            if (u < steps[w]) ok = issue_s(w, u);
-        for (int u = 0; u < steps[w0] && ok; ++u)
-          for (int w = w0; w < w1 && ok; ++w) {
-            if (u >= steps[w]) continue;
-            ok = issue_pv(w, u);
-            if (ok && u + C::kBufs < steps[w]) ok = issue_s(w, u + C::kBufs);
-            if (ok) release_v(w, u);
-          }
-        for (int w = w0; w < w1; ++w) {
-          uu[w] += steps[w];
-          segs[w] += steps[w] > 0;
-        }
-        e0 += 2 * (g.k1 - g.k0);
-      }
-      if (leader) mma_commit(&bar.drained[w0]);
-      __syncwarp();
-      mbar_wait_drain(&bar.drained[w0], 0, p.err);
-    }
-  } else {
-    reg_alloc<kRegsHigh>();
-    // ------------------------------------------------------------------ softmax of stream w
-    const int w = (warp - 4) >> 2, wq = warp & 3;
-    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_base = tmem + lane_base + w * 128, o_col = tmem + lane_base + 256 + w * D;
-    const float c = p.scale_log2;
-    int uu = 0, segs = 0;
+  } else if (warp == 1) {
+    reg_dealloc<C::kRegsLow>();
+    // ------------------------------------------------------------------ products
+    const uint32_t idesc_s = idesc_f16kind(1, kTile, kTile, 0, 0);
+    const uint32_t idesc_o = idesc_f16kind(1, kTile, D, 0, 1);
+    // addresses stay below 2^18: an offset adds to the descriptor's address field
+    const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
+    const uint64_t k_desc = sw128_desc(smem_u32(kv_s), 16, C::kHalves * 1024);
+    const uint64_t v_desc = sw128_desc(smem_u32(kv_s), 1024, C::kHalves * 1024);
+    const bool leader = elect_one();           // the warp waits, one lane issues
+    int e0 = 0, slot = 0, used[2] = {0, 0};    // first ring entry of the segment, next query slot
+    int done[2] = {0, 0}, segs[2] = {0, 0};    // steps and segments of each stream
     bool ok = true;
     for (int sg = 0;; ++sg) {
       Segment g;
       ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
       if (!ok || g.nk == 0) break;
       const bool two = g.two;
-      const int steps = stream_steps(two, w, (g.k1 - g.k0) * C::kPerTile);
+      const int n = g.k1 - g.k0;
+      const int steps[2] = {stream_steps(two, 0, n), stream_steps(two, 1, n)};
+      const int qs[2] = {slot, two ? slot ^ 1 : slot};
+      ok = mbar_wait_bounded(&bar.q_full[slot], used[slot] & 1, abort, p.err);
+      if (two) ok = ok && mbar_wait_bounded(&bar.q_full[slot ^ 1], used[slot ^ 1] & 1, abort, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      ++used[slot];
+      if (two) ++used[slot ^ 1];
+      else slot ^= 1;
+      // Stream w's step u takes key tile two ? u : 2 u + w. Stream 1 comes after stream 0: its product
+      // frees a tile that both use, and finds it waited for.
+      auto stage = [&](int w, int u, int kv) { return (e0 + 2 * (two ? u : 2 * u + w) + kv) % C::kStages; };
+      auto landed = [&](int w, int u, int kv) {
+        if (two && w == 1) return true;
+        const int e = e0 + 2 * (two ? u : 2 * u + w) + kv;
+        return mbar_wait_bounded(&bar.full[e % C::kStages], (e / C::kStages) & 1, abort, p.err);
+      };
+      auto weighed = [&](int w, int u) {       // P of step u stands, and O may be written
+        if (u == 0 && segs[w] > 0 && !mbar_wait_bounded(&bar.o_free[w], (segs[w] - 1) & 1, abort, p.err)) return false;
+        return mbar_wait_bounded(&bar.p_full[w], (done[w] + u) & 1, abort, p.err);
+      };
+      auto score = [&](int w, int u) {         // S = Q K^T
+        const int st = stage(w, u, 0);
+        const uint64_t qd = q_desc + (qs[w] * C::kTileBytes >> 4), kd = k_desc + (st * C::kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          mma_ss(tmem + w * 128, qd + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4),
+                 kd + (((c >> 2) * 1024 + (c & 3) * 32) >> 4), idesc_s, c > 0 ? 1u : 0u);
+        mma_commit(&bar.s_full[w]);
+        if (w == 1 || !two) mma_commit(&bar.empty[st]);
+        // the last product that reads these queries
+        if (two ? u + 1 == steps[w] : 2 * u + w + 1 == n) mma_commit(&bar.q_empty[qs[w]]);
+      };
+      auto add_v = [&](int w, int u) {         // O += P V
+        const uint64_t vd = v_desc + (stage(w, u, 1) * C::kTileBytes >> 4);
+#pragma unroll
+        for (int j = 0; j < C::kSub; ++j)
+#pragma unroll
+          for (int c = 0; c < C::kCols / 16; ++c)
+            mma_ts(tmem + 256 + (w * C::kSub + j) * D, tmem + w * 128 + j * 64 + c * 8,
+                   vd + ((j * C::kCols + c * 16) * (D * 2) >> 4), idesc_o, u > 0 || c > 0 ? 1u : 0u);
+        if (u + 1 == steps[w]) mma_commit(&bar.o_full[w]);
+      };
+      auto free_v = [&](int w, int u) {
+        if (w == 1 || !two) mma_commit(&bar.empty[stage(w, u, 1)]);
+      };
+      for (int w = 0; w < 2 && ok; ++w)
+        if (steps[w] > 0) {
+          ok = __all_sync(0xffffffffu, landed(w, 0, 0));
+          tc_fence_after();
+          if (ok && leader) score(w, 0);
+          __syncwarp();
+        }
+      if (C::kSub == 2 && two) {
+        // products of 64 columns take no longer than their issue: P V of a step and the next S go out
+        // back to back, behind all of their waits (with a wait between them 627 for 676 TFLOP/s)
+        for (int u = 0; u < n && ok; ++u) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const bool more = u + 1 < n;
+            ok = ok && __all_sync(0xffffffffu, landed(w, u, 1) && (!more || landed(w, u + 1, 0)) && weighed(w, u));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              add_v(w, u);
+              if (more) score(w, u + 1);
+              free_v(w, u);
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        // S of the next step as soon as its keys are there
+        for (int u = 0; u < steps[0] && ok; ++u)
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (u >= steps[w]) continue;
+            ok = __all_sync(0xffffffffu, landed(w, u, 1) && weighed(w, u));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) add_v(w, u);
+            __syncwarp();
+            if (u + 1 < steps[w]) {
+              ok = __all_sync(0xffffffffu, landed(w, u + 1, 0));
+              if (!ok) break;
+              if (leader) score(w, u + 1);
+              __syncwarp();
+            }
+            if (leader) free_v(w, u);
+            __syncwarp();
+          }
+      }
+      for (int w = 0; w < 2; ++w) {
+        done[w] += steps[w];
+        segs[w] += steps[w] > 0;
+      }
+      e0 += 2 * n;
+    }
+    if (leader) mma_commit(&bar.drained);
+    __syncwarp();
+    mbar_wait_drain(&bar.drained, 0, p.err);
+  } else if (warp == 2) {
+    reg_dealloc<C::kRegsLow>();                // gives up registers, nothing else
+  } else {
+    reg_alloc<C::kRegsHigh>();
+    // ------------------------------------------------------------------ softmax: stream w, keys j of a tile
+    const int group = (warp - 4) >> 2, w = group / C::kSub, j = group % C::kSub, wq = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + w * 128 + j * 64;
+    const uint32_t o_col = tmem + lane_base + 256 + group * D;
+    const float c = p.scale_log2;
+    int done = 0, segs = 0;
+    bool ok = true;
+    for (int sg = 0;; ++sg) {
+      Segment g;
+      ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
+      if (!ok || g.nk == 0) break;
+      const bool two = g.two;
+      const int steps = stream_steps(two, w, g.k1 - g.k0);
       const int t0 = g.i * p.item_tokens + (two ? w * p.tile_tokens : 0);
       const int rows = min(p.tile_tokens, g.v.n - t0) * p.G;
       const int r = wq * 32 + lane;
       const int tok = t0 + r / p.G;
-      const int hq = g.h * p.G + r % p.G;
       const bool active = wq * 32 < rows;      // this warp has rows
       // rows of nobody compute what nobody reads: they mask nothing and move nothing
       const int limit = r < rows ? key_limit(p, g.b, g.v, tok) : 1 << 30;
       float m = -INFINITY, l = 0.f;
       for (int u = 0; u < steps; ++u) {
-        const int x = (uu + u) % C::kBufs;
-        const uint32_t s_col = s_base + x * C::kStep;
-        ok = mbar_wait_bounded(&bar.s_full[w][x], ((uu + u) / C::kBufs) & 1, abort, p.err);
+        ok = mbar_wait_bounded(&bar.s_full[w], (done + u) & 1, abort, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          const int bk = two ? u : 2 * u + w;
-          uint32_t s[C::kStep];
+          uint32_t s[C::kCols];
 #pragma unroll
-          for (int q = 0; q < C::kStep / 32; ++q)
+          for (int q = 0; q < C::kCols / 32; ++q)
             tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-          const KeyTile kt = key_tile_at(p, g, g.k0 + bk / C::kPerTile);
-          const int valid = (kt.b == g.b ? limit : kt.len) - kt.key0 - (bk % C::kPerTile) * C::kStep;
-          const bool masked = __any_sync(0xffffffffu, valid < C::kStep);
+          const KeyTile kt = key_tile_at(p, g, g.k0 + (two ? u : 2 * u + w));
+          const int valid = (kt.b == g.b ? limit : kt.len) - kt.key0 - j * C::kCols;
+          const bool masked = __any_sync(0xffffffffu, valid < C::kCols);
           tmem_ld_wait();
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < C::kStep; ++k)
+            for (int k = 0; k < C::kCols; ++k)
               if (k >= valid) s[k] = 0xff800000u;
           }
           // the row's reference maximum moves when a weight would pass 2^8, or on a NaN
@@ -449,22 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = move ? ex2(m - m_new) : 1.f;           // 0 from -inf
             l *= f;
             m = m_new;
-            if (u > 0) {
-              if (C::kBufs > 1) {
-                // S is ahead of O here: the product of the step before must be done
-                ok = mbar_wait_bounded(&bar.pv_done[w], (uu + u - 1) & 1, abort, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-              }
+            if (u > 0) {                       // S of this step is complete, and so the product of the last
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(o_col + 32 * q, o);
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(o_col + 16 * q, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(o_col + 32 * q, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(o_col + 16 * q, o);
               }
             }
           }
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t c2 = pk2(c, c), nm2 = pk2(-base, -base);
           uint32_t pb[32];
 #pragma unroll
-          for (int q = 0; q < C::kStep / 64; ++q) {
+          for (int q = 0; q < C::kCols / 64; ++q) {
             l += masked ? weigh<0>(&s[64 * q], c2, nm2, pb) : weigh<C::kPoly8>(&s[64 * q], c2, nm2, pb);
             tmem_st32(s_col + 32 * q, pb);
           }
@@ -480,23 +484,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[w][x]);
+        if (lane == 0) mbar_arrive(&bar.p_full[w]);
       }
       if (!ok) break;
-      uu += steps;
+      done += steps;
+      const int hq = g.h * p.G + r % p.G;
       const bool whole = g.k0 == 0 && g.k1 == g.nk && two && writes_rows(p, g.v, g.i);
       const long long out = static_cast<long long>(g.v.r0 + tok) * p.Hq + hq;
       const long long slot = g.k0 == 0 ? row_slot(p, g.b, two ? 0 : w, g.v.r0 + tok, hq)
                                        : cta_slot(p, blockIdx.x, w * kTile + r);
-      if (r < rows) {
-        if (!whole) p.part_ml[slot] = make_float2(m, l);
-        else if (p.lse) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+      if (steps == 0) {
+        if (j == 0 && r < rows) p.part_ml[slot] = make_float2(m, l);
+        continue;
       }
-      if (steps == 0) continue;
       ok = mbar_wait_bounded(&bar.o_full[w], segs & 1, abort, p.err);
+      // the second warpgroup's results go to the first through shared memory
+      if (C::kSub == 2 && j == 1 && segs > 0)
+        ok = ok && mbar_wait_bounded(&bar.x_empty[w], (segs - 1) & 1, abort, p.err);
+      if (C::kSub == 2 && j == 0) ok = ok && mbar_wait_bounded(&bar.x_full[w], segs & 1, abort, p.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      float4* mate = join_o + w * (kTile * D / 4) + r;
+      float own = 1.f, other = 0.f;            // factors of the two warpgroups' results
+      if (C::kSub == 2) {
+        if (j == 1) {
+          join_ml[w * kTile + r] = make_float2(m, l);
+        } else {
+          const float2 ml = join_ml[w * kTile + r];
+          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+          own = ex2(m - base);
+          other = ex2(ml.x - base);
+          l = l * own + ml.y * other;
+          m = top;
+        }
+      }
+      if (j == 0 && r < rows) {
+        if (!whole) p.part_ml[slot] = make_float2(m, l);
+        else if (p.lse) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+      }
       if (active) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -504,30 +530,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(o_col + 32 * q, o);
           tmem_ld_wait();
-          if (r >= rows) {
-          } else if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D + 32 * q);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t y[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                y[j] = pack_bf16(__uint_as_float(o[8 * k + 2 * j]) * inv, __uint_as_float(o[8 * k + 2 * j + 1]) * inv);
-              dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + 32 * q);
+          if (C::kSub == 2 && j == 1) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                   __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+              mate[(8 * q + k) * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                      __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          } else {
+            if (C::kSub == 2) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 x = mate[(8 * q + k) * kTile];
+                o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * own + x.x * other);
+                o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * own + x.y * other);
+                o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * own + x.z * other);
+                o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * own + x.w * other);
+              }
+            }
+            if (r < rows && whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D + 32 * q);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y[i] = pack_bf16(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+                dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else if (r < rows) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + 32 * q);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            }
           }
           __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.o_free[w]);
+      if (lane == 0) {
+        if (C::kSub == 2) mbar_arrive(j == 1 ? &bar.x_full[w] : &bar.x_empty[w]);
+        mbar_arrive(&bar.o_free[w]);
+      }
       ++segs;
     }
   }
@@ -539,17 +584,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int SUB>
 cudaError_t launch(cudaStream_t s, const PagedParams& p, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v) {
+  using C = Cfg<D, SUB>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_tc_kernel<D>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_tc_kernel<D, SUB>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   return e != cudaSuccess ? e
-                          : launch_pdl(paged_attend_tc_kernel<D>, dim3(p.grid), dim3(kThreads), Cfg<D>::kSmem, s, q, k,
-                                       v, p);
+                          : launch_pdl(paged_attend_tc_kernel<D, SUB>, dim3(p.grid), dim3(C::kThreads), C::kSmem, s, q,
+                                       k, v, p);
 }
 
 }  // namespace
@@ -558,7 +604,10 @@ cudaError_t launch_paged_attend_tc(cudaStream_t s, const PagedParams& p) {
   CUtensorMap q, k, v;
   if (!encode_rows_tmap(&q, p.q, p) || !encode_slots_tmap(&k, p.k_pool, p) || !encode_slots_tmap(&v, p.v_pool, p))
     return cudaErrorInvalidValue;
-  return p.D == 64 ? launch<64>(s, p, q, k, v) : launch<128>(s, p, q, k, v);
+  if (p.D == 128) return launch<128, 1>(s, p, q, k, v);
+  // the sequences' rows fill more than a tile, on average
+  const bool many = p.rows > static_cast<long long>(p.B) * p.tile_tokens;
+  return many ? launch<64, 2>(s, p, q, k, v) : launch<64, 1>(s, p, q, k, v);
 }
 
 }  // namespace kvc
