@@ -95,22 +95,24 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   if (b->dtype == KVC_BF16) {
     // two tiles of 128 packed rows share a CTA's key tiles
     p->tile_tokens = 128 / p->G;
-    p->item_tokens = 2 * p->tile_tokens;
+    p->item_tokens = p->prefix_item_tokens = 2 * p->tile_tokens;
     p->key_tile = 128;
     p->streams = 2;
     p->slot_rows = 256;
     p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens;
     return;
   }
-  // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend
-  // its products on padding), else of 64
-  const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
-  p->slot_rows = per_seq <= 16 ? 16 : 64;
-  p->tile_tokens = p->item_tokens = p->slot_rows / p->G;
+  // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend its
+  // products on padding), else of 64; the prefix's by the batch's rows
+  const long long all = static_cast<long long>(p->rows) * p->G;
+  const int few = (all + p->B - 1) / p->B <= 16 ? 16 : 64;
+  p->tile_tokens = p->item_tokens = few / p->G;
+  p->prefix_item_tokens = (all <= 16 ? 16 : 64) / p->G;
+  p->slot_rows = all <= 16 ? 16 : 64;
   p->key_tile = 64;
   p->streams = 1;
-  p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens;
-  p->grid *= 2;
+  p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens && few == 64;
+  if (p->D == 64) p->grid *= 2;                // CTAs that fit an SM
 }
 
 void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
@@ -307,11 +309,11 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     const SeqView v = seq_view(p, s);
     const int t = row - v.r0;
     if (t < 0 || t >= v.n) return;
-    const int item = t / p.item_tokens, in = t - item * p.item_tokens;
+    const int it = item_tokens(p, s), item = t / it, in = t - item * it;
     nk = item_units(p, s, v, item);
     first = h * head_units(p, s, v) + units_before(p, s, v, item);
     split = p.streams == 2 && v.n - item * p.item_tokens <= p.tile_tokens;
-    tile = in / p.tile_tokens;
+    tile = p.streams == 2 ? in / p.tile_tokens : 0;
     at = (in - tile * p.tile_tokens) * p.G + g;
     whole = writes_rows(p, v, item);
   };

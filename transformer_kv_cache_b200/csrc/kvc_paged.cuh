@@ -46,7 +46,8 @@ struct PagedParams {
   int* err;
   // schedule
   int item_tokens;              // query tokens of an item
-  int tile_tokens;              // query tokens of a tile (item_tokens, or half of it)
+  int prefix_item_tokens;       // the same for the prefix's items
+  int tile_tokens;              // query tokens of a tile (the item's, or half of them)
   int key_tile;                 // keys of a unit
   int prefix_units;             // key tiles of the prefix
   int streams;                  // tiles of an item: 1, or 2 (an item of one tile splits its keys in two streams)
@@ -82,8 +83,12 @@ __device__ __forceinline__ void seq_check(const PagedParams& p, int b) {
   if (lo < 0 || hi < lo || hi > p.rows || len < 0 || len > paged_cap(p)) latch_error(p.err, DERR_BOUNDS);
 }
 
-__device__ __forceinline__ int seq_items(const PagedParams& p, const SeqView& v) {
-  return (v.n + p.item_tokens - 1) / p.item_tokens;
+__device__ __forceinline__ int item_tokens(const PagedParams& p, int b) {
+  return b < 0 ? p.prefix_item_tokens : p.item_tokens;
+}
+__device__ __forceinline__ int seq_items(const PagedParams& p, int b, const SeqView& v) {
+  const int it = item_tokens(p, b);
+  return (v.n + it - 1) / it;
 }
 // Key tiles of the prefix that each item reads before its own (p.join).
 __device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return p.join ? p.prefix_units : 0; }
@@ -92,7 +97,7 @@ __device__ __forceinline__ int keys_before(const PagedParams& p, int b, const Se
   return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t)) : v.len;
 }
 __device__ __forceinline__ int item_units(const PagedParams& p, int b, const SeqView& v, int i) {
-  const int t = min(v.n, (i + 1) * p.item_tokens);
+  const int t = min(v.n, (i + 1) * item_tokens(p, b));
   return prefix_tiles(p) + (keys_before(p, b, v, t) + p.key_tile - 1) / p.key_tile;
 }
 // sum over j < n of floor((a j + b) / m), for a, b >= 0: whole multiples of m come out in closed
@@ -120,7 +125,7 @@ __device__ __forceinline__ long long units_before(const PagedParams& p, int b, c
   if (i <= 0) return 0;
   if (b < 0 || !p.causal) return static_cast<long long>(i) * item_units(p, b, v, 0);
   // items before the last see len - n + (j + 1) item_tokens keys, none while that is negative
-  const int whole = min(i, seq_items(p, v) - 1);
+  const int whole = min(i, seq_items(p, b, v) - 1);
   const int it = p.item_tokens, first = v.len - v.n;
   const int skip = first < 0 ? min(whole, -first / it) : 0;
   long long s = static_cast<long long>(i) * prefix_tiles(p);
@@ -129,7 +134,7 @@ __device__ __forceinline__ long long units_before(const PagedParams& p, int b, c
   return s;
 }
 __device__ __forceinline__ long long head_units(const PagedParams& p, int b, const SeqView& v) {
-  return units_before(p, b, v, seq_items(p, v));
+  return units_before(p, b, v, seq_items(p, b, v));
 }
 
 // The schedule's walk through a CTA's units.
@@ -158,7 +163,7 @@ struct Walk {
 };
 __device__ __forceinline__ void walk_to(const PagedParams& p, Walk& w, int b) {
   w.b = b;
-  w.items = seq_items(p, w.v);
+  w.items = seq_items(p, b, w.v);
   if (b + 1 < p.B) w.next = seq_view(p, b + 1);
 }
 
@@ -276,7 +281,7 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segm
     g.k0 = static_cast<int>(w.u - w.item_first);
     g.k1 = static_cast<int>(min(static_cast<long long>(nk), w.u1 - w.item_first));
     g.nk = nk;
-    g.two = w.v.n - w.i * p.item_tokens > p.tile_tokens;
+    g.two = p.streams == 2 && w.v.n - w.i * p.item_tokens > p.tile_tokens;
     w.u = w.item_first + g.k1;
     return true;
   }

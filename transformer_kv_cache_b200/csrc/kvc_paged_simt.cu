@@ -3,7 +3,9 @@
 //
 // Attention: one pass over an item's keys with the running maximum and sum of the softmax; 256
 // threads as 16 x 16, a thread holding ROWS / 16 query rows by 4 keys of the scores and
-// ROWS / 16 rows by D / 16 columns of the output in registers. Weights: the same products with
+// ROWS / 16 rows by D / 16 columns of the output in registers; the next tile's keys and values
+// arrive by cp.async under this one's products. A tile is 16 rows where sequences have no more,
+// else 64, the prefix's chosen by the batch's rows. Weights: the same products with
 // keys and rows exchanged, so that a key's sum over the query rows stays in one half-warp.
 #include <math_constants.h>
 
@@ -71,118 +73,181 @@ __device__ __forceinline__ void dots(const float* a, int lda, int sa, const floa
   }
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const PagedParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
+// 16 bytes to shared memory behind the registers' back, or zeros where `there` is false.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+
+// A CTA's loads of key tiles: a thread copies the same 16 bytes of kKeys of a tile's keys, whose
+// pages it asks for one tile ahead.
+template <int D>
+struct KeyLoader {
+  static constexpr int kChunks = D / 4, kKeys = kKT * kChunks / kThreads, kStep = kThreads / kChunks;
+  int page[kKeys];
+  KeyTile tile;
+
+  __device__ __forceinline__ void look(const PagedParams& p, const Segment& g, int kt) {
+    tile = key_tile_at(p, g, kt);
+    const int32_t* table =
+        tile.b < 0 ? p.prefix_pages : p.page_table + static_cast<long long>(tile.b) * p.max_pages;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int key = tile.key0 + static_cast<int>(threadIdx.x) / kChunks + i * kStep;
+      page[i] = key < tile.len ? __ldg(table + (key >> p.page_shift)) : -1;
+    }
+  }
+  __device__ __forceinline__ void load(const PagedParams& p, int h, float* ks, float* vs, int ld) const {
+    const int c = static_cast<int>(threadIdx.x) % kChunks;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int at = static_cast<int>(threadIdx.x) / kChunks + i * kStep, key = tile.key0 + at;
+      const bool in = key < tile.len, there = in && page[i] >= 0 && page[i] < p.pool_pages;
+      if (in && !there) latch_error(p.err, DERR_BOUNDS);
+      const long long row = there ? ((static_cast<long long>(page[i]) * p.Hkv + h) << p.page_shift) +
+                                        (key & ((1 << p.page_shift) - 1))
+                                  : 0;
+      cp_async16_or_zero(ks + at * ld + c * 4, static_cast<const float*>(p.k_pool) + row * D + c * 4, there);
+      cp_async16_or_zero(vs + at * ld + c * 4, static_cast<const float*>(p.v_pool) + row * D + c * 4, there);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
+// One segment in tiles of ROWS query rows; sm holds [rows][LD] queries, two stages of [kKT][LD] keys
+// and values, [rows][LP] weights.
+template <int D, int ROWS, int MAXROWS>
+__device__ __forceinline__ void attend_segment(const PagedParams& p, const Segment& g, float* sm) {
   constexpr int LD = D + 4, RPT = ROWS / 16, LP = kKT + 4;
-  extern __shared__ float sm[];
-  float* qs = sm;                              // [ROWS][LD]
-  float* ks = qs + ROWS * LD;                  // [kKT][LD]
-  float* vs = ks + kKT * LD;                   // [kKT][LD]
-  float* ps = vs + kKT * LD;                   // [ROWS][LP]
-  __shared__ long long plan_s[kPlanWords + kThreads / 32];
+  float* qs = sm;
+  float* kv = qs + MAXROWS * LD;               // [stage][K, V][kKT][LD]
+  float* ps = kv + 4 * kKT * LD;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  Walk w = plan_walk(p, plan_s, [&](int b, const SeqView& v) { return head_units(p, b, v); });
-  walk_to_item(p, w);
-  Segment g;
-  while (next_segment(p, w, g)) {
-    const int t0 = g.i * p.item_tokens;
-    const int tokens = min(p.item_tokens, g.v.n - t0), rows = tokens * p.G;
+  const int t0 = g.i * item_tokens(p, g.b);
+  const int tokens = min(item_tokens(p, g.b), g.v.n - t0), rows = tokens * p.G;
+  KeyLoader<D> loader;
+  loader.look(p, g, g.k0);
+  __syncthreads();                             // the segment before is read
+  loader.load(p, g.h, kv, kv + kKT * LD, LD);
+  load_queries<D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
+  float m[RPT], l[RPT], acc[RPT][D / 16];
+  int limit[RPT];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.f;
+    const int at = ty * RPT + r;
+    limit[r] = at < rows ? key_limit(p, g.b, g.v, t0 + at / p.G) : 0;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
+  }
+  if (g.k0 + 1 < g.k1) loader.look(p, g, g.k0 + 1);
+  for (int kt = g.k0; kt < g.k1; ++kt) {
+    const int st = (kt - g.k0) & 1;
+    const float* ks = kv + st * 2 * kKT * LD;
+    const float* vs = ks + kKT * LD;
+    if (kt + 1 < g.k1) {
+      float* next = kv + (st ^ 1) * 2 * kKT * LD;
+      loader.load(p, g.h, next, next + kKT * LD, LD);
+      if (kt + 2 < g.k1) loader.look(p, g, kt + 2);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
     __syncthreads();
-    load_queries<D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
-    float m[RPT], l[RPT], acc[RPT][D / 16];
-    int limit[RPT];
+    const KeyTile tile = key_tile_at(p, g, kt);
+    float s[RPT][4];
+    dots<D, RPT, 4>(qs + ty * RPT * LD, LD, 1, ks + tx * LD, LD, 16, s);
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-      m[r] = -CUDART_INF_F;
-      l[r] = 0.f;
-      const int at = ty * RPT + r;
-      limit[r] = at < rows ? key_limit(p, g.b, g.v, t0 + at / p.G) : 0;
+      float mx = -CUDART_INF_F;
+      const int end = (tile.b == g.b ? limit[r] : tile.len) - tile.key0;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
-    }
-    for (int kt = g.k0; kt < g.k1; ++kt) {
-      const KeyTile tile = key_tile_at(p, g, kt);
-      __syncthreads();
-      load_keys<D, LD>(p, p.k_pool, tile.b, g.h, tile.key0, tile.len, ks);
-      load_keys<D, LD>(p, p.v_pool, tile.b, g.h, tile.key0, tile.len, vs);
-      __syncthreads();
-      float s[RPT][4];
-      dots<D, RPT, 4>(qs + ty * RPT * LD, LD, 1, ks + tx * LD, LD, 16, s);
-#pragma unroll
-      for (int r = 0; r < RPT; ++r) {
-        float mx = -CUDART_INF_F;
-        const int end = (tile.b == g.b ? limit[r] : tile.len) - tile.key0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[r][j] = tx + 16 * j < end ? s[r][j] * p.scale_log2 : -CUDART_INF_F;
-          mx = fmaxf(mx, s[r][j]);
-        }
-#pragma unroll
-        for (int d = 8; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float m_new = fmaxf(m[r], mx);
-        const float base = m_new == -CUDART_INF_F ? 0.f : m_new;   // nothing visible yet: every weight is 0
-        const float f = exp2f(m[r] - base);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(s[r][j] - base);
-          sum += e;
-          ps[(ty * RPT + r) * LP + tx + 16 * j] = e;
-        }
-#pragma unroll
-        for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l[r] = l[r] * f + sum;
-        m[r] = m_new;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[r][c] *= f;
+      for (int j = 0; j < 4; ++j) {
+        s[r][j] = tx + 16 * j < end ? s[r][j] * p.scale_log2 : -CUDART_INF_F;
+        mx = fmaxf(mx, s[r][j]);
       }
-      __syncwarp();                            // a row's weights are written and read by one half-warp
-      for (int k = 0; k < kKT; k += 4) {
-        float4 pr[RPT];
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) pr[r] = load4(ps + (ty * RPT + r) * LP + k);
+      for (int d = 8; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float m_new = fmaxf(m[r], mx);
+      const float base = m_new == -CUDART_INF_F ? 0.f : m_new;     // nothing visible yet: every weight is 0
+      const float f = exp2f(m[r] - base);
+      float sum = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[r][j] - base);
+        sum += e;
+        ps[(ty * RPT + r) * LP + tx + 16 * j] = e;
+      }
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const float4 v4 = load4(vs + (k + kk) * LD + c * 64 + tx * 4);
+      for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[r] = l[r] * f + sum;
+      m[r] = m_new;
 #pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-              const float e = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
-              acc[r][4 * c + 0] = fmaf(e, v4.x, acc[r][4 * c + 0]);
-              acc[r][4 * c + 1] = fmaf(e, v4.y, acc[r][4 * c + 1]);
-              acc[r][4 * c + 2] = fmaf(e, v4.z, acc[r][4 * c + 2]);
-              acc[r][4 * c + 3] = fmaf(e, v4.w, acc[r][4 * c + 3]);
-            }
+      for (int c = 0; c < D / 16; ++c) acc[r][c] *= f;
+    }
+    __syncwarp();                              // a row's weights are written and read by one half-warp
+#pragma unroll 2
+    for (int k = 0; k < kKT; k += 4) {
+      float4 pr[RPT];
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) pr[r] = load4(ps + (ty * RPT + r) * LP + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const float4 v4 = load4(vs + (k + kk) * LD + c * 64 + tx * 4);
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) {
+            const float e = kk == 0 ? pr[r].x : kk == 1 ? pr[r].y : kk == 2 ? pr[r].z : pr[r].w;
+            acc[r][4 * c + 0] = fmaf(e, v4.x, acc[r][4 * c + 0]);
+            acc[r][4 * c + 1] = fmaf(e, v4.y, acc[r][4 * c + 1]);
+            acc[r][4 * c + 2] = fmaf(e, v4.z, acc[r][4 * c + 2]);
+            acc[r][4 * c + 3] = fmaf(e, v4.w, acc[r][4 * c + 3]);
           }
         }
       }
     }
+    __syncthreads();                           // the stage is read
+  }
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-      const int at = ty * RPT + r;
-      if (at >= rows) continue;
-      if (g.k0 == 0 && g.k1 == g.nk && writes_rows(p, g.v, g.i)) {
-        const long long out = static_cast<long long>(g.v.r0 + t0 + at / p.G) * p.Hq + g.h * p.G + at % p.G;
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-        if (p.lse && tx == 0) p.lse[out] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * D + c * 64 + tx * 4) =
-              make_float4(acc[r][4 * c] * inv, acc[r][4 * c + 1] * inv, acc[r][4 * c + 2] * inv,
-                          acc[r][4 * c + 3] * inv);
-        continue;
-      }
-      const long long slot = g.k0 == 0 ? row_slot(p, g.b, 0, g.v.r0 + t0 + at / p.G, g.h * p.G + at % p.G)
-                                       : cta_slot(p, blockIdx.x, at);
-      if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);
+  for (int r = 0; r < RPT; ++r) {
+    const int at = ty * RPT + r;
+    if (at >= rows) continue;
+    if (g.k0 == 0 && g.k1 == g.nk && writes_rows(p, g.v, g.i)) {
+      const long long out = static_cast<long long>(g.v.r0 + t0 + at / p.G) * p.Hq + g.h * p.G + at % p.G;
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+      if (p.lse && tx == 0) p.lse[out] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
-        *reinterpret_cast<float4*>(p.part_o + slot * D + c * 64 + tx * 4) =
-            make_float4(acc[r][4 * c], acc[r][4 * c + 1], acc[r][4 * c + 2], acc[r][4 * c + 3]);
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * D + c * 64 + tx * 4) =
+            make_float4(acc[r][4 * c] * inv, acc[r][4 * c + 1] * inv, acc[r][4 * c + 2] * inv, acc[r][4 * c + 3] * inv);
+      continue;
     }
+    const long long slot = g.k0 == 0 ? row_slot(p, g.b, 0, g.v.r0 + t0 + at / p.G, g.h * p.G + at % p.G)
+                                     : cta_slot(p, blockIdx.x, at);
+    if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<float4*>(p.part_o + slot * D + c * 64 + tx * 4) =
+          make_float4(acc[r][4 * c], acc[r][4 * c + 1], acc[r][4 * c + 2], acc[r][4 * c + 3]);
+  }
+}
+
+// OWN and PREFIX: query rows of a tile of a sequence's own keys and of the prefix's.
+template <int D, int OWN, int PREFIX>
+__global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const PagedParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  extern __shared__ __align__(16) float sm[];
+  __shared__ long long plan_s[kPlanWords + kThreads / 32];
+  constexpr int kMax = OWN > PREFIX ? OWN : PREFIX;
+  Walk w = plan_walk(p, plan_s, [&](int b, const SeqView& v) { return head_units(p, b, v); });
+  walk_to_item(p, w);
+  Segment g;
+  while (next_segment(p, w, g)) {
+    if (OWN != PREFIX && g.b < 0) attend_segment<D, PREFIX, kMax>(p, g, sm);
+    else attend_segment<D, OWN, kMax>(p, g, sm);
   }
 }
 
@@ -244,15 +309,24 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   }
 }
 
-template <int D, int ROWS>
+template <int D, int OWN, int PREFIX>
 cudaError_t attend(cudaStream_t s, const PagedParams& p) {
-  constexpr size_t smem = sizeof(float) * (ROWS * (D + 4) + 2 * kKT * (D + 4) + ROWS * (kKT + 4));
+  constexpr int kMax = OWN > PREFIX ? OWN : PREFIX;
+  constexpr size_t smem = sizeof(float) * (kMax * (D + 4) + 4 * kKT * (D + 4) + kMax * (kKT + 4));
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<D, ROWS>),
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<D, OWN, PREFIX>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
-  return e != cudaSuccess ? e : launch_pdl(paged_attend_simt_kernel<D, ROWS>, dim3(p.grid), dim3(kThreads), smem, s, p);
+  return e != cudaSuccess
+             ? e
+             : launch_pdl(paged_attend_simt_kernel<D, OWN, PREFIX>, dim3(p.grid), dim3(kThreads), smem, s, p);
+}
+template <int D>
+cudaError_t attend(cudaStream_t s, const PagedParams& p) {
+  const bool own16 = p.item_tokens * p.G <= 16, prefix16 = p.prefix_item_tokens * p.G <= 16;
+  if (!own16) return attend<D, 64, 64>(s, p);
+  return prefix16 ? attend<D, 16, 16>(s, p) : attend<D, 16, 64>(s, p);
 }
 template <int D, int ROWS>
 cudaError_t weights(cudaStream_t s, const PagedParams& p) {
@@ -269,9 +343,7 @@ cudaError_t weights(cudaStream_t s, const PagedParams& p) {
 }  // namespace
 
 cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p) {
-  const bool few = p.slot_rows == 16;
-  if (p.D == 64) return few ? attend<64, 16>(s, p) : attend<64, 64>(s, p);
-  return few ? attend<128, 16>(s, p) : attend<128, 64>(s, p);
+  return p.D == 64 ? attend<64>(s, p) : attend<128>(s, p);
 }
 
 cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p) {
