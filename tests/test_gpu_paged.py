@@ -237,6 +237,9 @@ EVICTIONS = {
     "ragged": dict(lengths=[1000, 257, 511, 64, 2000], keep=200, sinks=4, recent=33),
     "half of a long one": dict(lengths=[9001], keep=4500, sinks=4, recent=100),
     "most of it": dict(lengths=[5000, 4097], keep=4096, sinks=0, recent=1),
+    "eight and nine": dict(lengths=[108, 109, 101], keep=100, sinks=2, recent=10),
+    "few of a long one": dict(lengths=[9003, 9000], keep=8999, sinks=2, recent=500),
+    "few, and no slot to spare": dict(lengths=[24, 32], keep=24, sinks=24, recent=0),
 }
 
 
@@ -428,3 +431,117 @@ def test_lengths_and_rows_out_of_range_are_reported(kvc):
         kvc.kvc_paged_append(batch, c.q, c.q, c.row_start)
         torch.cuda.synchronize()
         assert int(c.error) == 3, change
+
+
+def test_log_sum_exp_that_is_no_number(kvc):
+    """Rows with an LSE of +inf add exactly nothing; a NaN reaches the tokens that its row sees."""
+    for dtype in DTYPES:
+        t, _ = build(dict(rows=[64, 70], lengths=[200, 333], hq=4, hkv=2, d=64), dtype, seed=17)
+        c = copy.deepcopy(t).to(DEV)
+        batch = c.handle(kvc)
+        work = c.workspace(kvc, batch)
+        lse = torch.full(c.q.shape[:2], math.inf, device=DEV)
+        kvc.kvc_paged_weights(batch, c.q, lse, c.row_start, work)
+        torch.cuda.synchronize()
+        assert torch.equal(c.scores.cpu(), t.scores)
+        _, real, _, _ = attend64(t, True)
+        lse = real.float().to(DEV)
+        lse[64 + 5] = math.nan                                # row 5 of sequence 1
+        kvc.kvc_paged_weights(batch, c.q, lse, c.row_start, work)
+        torch.cuda.synchronize()
+        bad = torch.isnan(c.scores.cpu())
+        want = torch.zeros_like(bad)
+        want[1, :, : 333 - 70 + 5 + 1] = True
+        assert torch.equal(bad, want)
+
+
+def test_not_a_number_stays_with_its_rows(kvc):
+    """A NaN or infinite query makes its own output NaN and no other row's."""
+    for dtype in DTYPES:
+        t, causal = build("chunks, causal", dtype, seed=18)
+        want = run_attend(kvc, t, causal)
+        t.q[3, 1, 7] = math.nan
+        t.q[250, 4, 0] = math.inf
+        got = run_attend(kvc, t, causal)
+        for x, y in zip(got, want):
+            differ = torch.isnan(x)
+            while differ.dim() > 2:
+                differ = differ.any(-1)
+            assert differ.nonzero().tolist() == [[3, 1], [250, 4]]
+            keep = ~differ
+            assert torch.equal(x[keep], y[keep])
+
+
+def test_no_rows_and_no_lse(kvc):
+    t, causal = build("decode, groups of 4", "bf16", seed=19)
+    want = run_attend(kvc, t, causal)
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    work = c.workspace(kvc, batch)
+    o = torch.empty_like(c.q)
+    kvc.kvc_paged_attend(batch, c.q, o, c.row_start, work, causal=causal)
+    none = c.q[:0]
+    zeros = torch.zeros_like(c.row_start)
+    kvc.kvc_paged_attend(batch, none, none, zeros, work)
+    kvc.kvc_paged_weights(batch, none, torch.empty(0, t.hq, device=DEV), zeros, work)
+    kvc.kvc_paged_append(batch, none[:, : t.hkv].contiguous(), none[:, : t.hkv].contiguous(), zeros)
+    torch.cuda.synchronize()
+    assert torch.equal(o.cpu(), want[0])
+    assert torch.equal(c.scores.cpu(), t.scores) and torch.equal(c.lengths.cpu(), t.lengths)
+
+
+def test_pages_past_two_to_the_31_elements(kvc):
+    """The last pages of a pool of 2.3 G elements give what the first ones of a small pool give."""
+    t = Batch(rows=[2], lengths=[150], hq=16, hkv=8, d=128, seed=20, room=20, stale=0.0, prefix=30)
+    small = copy.deepcopy(t).to(DEV)
+    far = copy.deepcopy(t).to(DEV)
+    pages, n = 140_000, t.k_pool.shape[0]
+    for name in ("k_pool", "v_pool"):
+        pool = torch.empty((pages,) + tuple(t.k_pool.shape[1:]), dtype=t.dtype, device=DEV)
+        pool[-n:] = getattr(far, name)
+        setattr(far, name, pool)
+    far.page_table += pages - n
+    far.prefix_pages += pages - n
+    assert far.k_pool[:-n].numel() > 2 ** 31
+    g = torch.Generator().manual_seed(2)
+    q, k, v = step_tensors(t, g, DEV)
+    results = []
+    for c in (small, far):
+        batch = c.handle(kvc)
+        work = c.workspace(kvc, batch, 100)
+        o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        kvc.kvc_paged_append(batch, k, v, c.row_start)
+        kvc.kvc_paged_attend(batch, q, o, c.row_start, work, lse=lse)
+        kvc.kvc_paged_weights(batch, q, lse, c.row_start, work)
+        kvc.kvc_paged_evict(batch, 100, 4, 16, work)
+        torch.cuda.synchronize()
+        assert int(c.error) == 0
+        results.append((o, lse, c.scores, c.positions, c.k_pool[-n:].clone(), c.v_pool[-n:].clone()))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_batches(kvc, dtype, seed):
+    """Random layouts: attention, then its weights, against fp64."""
+    g = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda *a: a[int(torch.randint(len(a), (1,), generator=g))]
+    upto = lambda n: int(torch.randint(n + 1, (1,), generator=g))
+    b, hkv, group = 1 + upto(8), pick(1, 2, 3, 4), pick(1, 2, 3, 5, 6, 8, 12, 17)
+    most = pick(1, 7, 130, 400)
+    lengths = [upto(pick(3, 60, 700, 2000)) for _ in range(b)]
+    causal = bool(upto(1))
+    t = Batch(rows=[upto(most) for _ in range(b - 1)] + [1 + upto(most)], lengths=lengths, hq=hkv * group, hkv=hkv,
+              d=pick(64, 128), page=pick(16, 32, 64, 128, 256), prefix=pick(0, 0, 5, 128, 300, 1111),
+              dtype=DTYPES[dtype], seed=seed, behind=upto(3))
+    o, lse = run_attend(kvc, t, causal)
+    check_attend(t, causal, o, lse)
+    total = int(t.row_start[-1])
+    lse[total:] = math.nan
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    kvc.kvc_paged_weights(batch, c.q, lse.to(DEV), c.row_start, c.workspace(kvc, batch), causal=causal)
+    torch.cuda.synchronize()
+    ref, bound = weights64(t, lse, causal)
+    assert ((c.scores.cpu().double() - ref).abs() <= bound).all()

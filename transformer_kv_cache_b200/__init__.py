@@ -448,6 +448,8 @@ def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, soft
     bf16), page_table int32 [sequences, pages of each], and the other arrays of include/kvc.h's
     struct. The struct keeps the tensors alive; the calls below read and write them in place."""
     import torch
+    if not getattr(k_pool, "is_cuda", False):
+        raise TypeError("k_pool: a CUDA tensor is expected here, not a host buffer")
     types = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}
     dev, i32 = k_pool.device, torch.int32
     if k_pool.dtype not in types or k_pool.dim() != 4:

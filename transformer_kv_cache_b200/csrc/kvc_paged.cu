@@ -105,7 +105,7 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   // tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend its
   // products on padding), else of 64; the prefix's by the batch's rows
   const long long all = static_cast<long long>(p->rows) * p->G;
-  const int few = (all + p->B - 1) / p->B <= 16 ? 16 : 64;
+  const int few = p->G <= 16 && (all + p->B - 1) / p->B <= 16 ? 16 : 64;
   p->tile_tokens = p->item_tokens = few / p->G;
   p->prefix_item_tokens = (all <= 16 ? 16 : 64) / p->G;
   p->slot_rows = all <= 16 ? 16 : 64;
