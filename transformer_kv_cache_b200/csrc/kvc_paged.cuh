@@ -143,6 +143,7 @@ struct Segment {
   SeqView v;
   int k0, k1, nk;               // key tiles [k0, k1) of the item's nk
   bool two;                     // the item has two tiles of query tokens
+  int phase;                    // which stream takes the first tile of an item that has one
 };
 // Key tile kt of an item: the sequence whose pages hold it (-1: the prefix), its first key there
 // and that sequence's keys.
@@ -306,14 +307,14 @@ __device__ __forceinline__ bool ring_put(SegmentRing& r, int k, const Segment& g
   if (k >= kRing && !mbar_wait_bounded(&r.empty[i], ((k / kRing) - 1) & 1, abort, err)) return false;
   r.a[i] = make_int4(g.b, g.h, g.i, g.two);
   r.b[i] = make_int4(g.v.r0, g.v.n, g.v.len, g.nk);
-  r.c[i] = make_int4(g.k0, g.k1, 0, 0);
+  r.c[i] = make_int4(g.k0, g.k1, g.phase, 0);
   mbar_arrive(&r.full[i]);
   return true;
 }
 __device__ __forceinline__ Segment ring_peek(const SegmentRing& r, int k) {
   const int i = k % kRing;
   const int4 a = r.a[i], b = r.b[i], c = r.c[i];
-  return {a.x, a.y, a.z, {b.x, b.y, b.z}, c.x, c.y, b.w, a.w != 0};
+  return {a.x, a.y, a.z, {b.x, b.y, b.z}, c.x, c.y, b.w, a.w != 0, c.z};
 }
 // The k-th segment out of it (a warp; the same answer in every lane).
 __device__ __forceinline__ bool ring_take(SegmentRing& r, int k, Segment& g, volatile int* abort, int* err) {

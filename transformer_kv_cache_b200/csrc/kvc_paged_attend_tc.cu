@@ -76,8 +76,24 @@ struct Bars {
   long long plan[kPlanWords + 20];
 };
 
-// Steps of stream w in a segment of n key tiles.
-__device__ __forceinline__ int stream_steps(bool two, int w, int n) { return two ? n : (n - w + 1) >> 1; }
+// The key tiles of stream w in a segment of n: all of them where the item has two tiles of rows,
+// else every other one (a segment of an odd number hands the next one's first
+// tile to the other stream, so that segments of a single tile keep both busy).
+__device__ __forceinline__ int stream_steps(const Segment& g, int w) {
+  return g.two ? g.k1 - g.k0 : (g.k1 - g.k0 - (w ^ g.phase) + 1) >> 1;
+}
+__device__ __forceinline__ int stream_tile(const Segment& g, int w, int u) {
+  return g.two ? u : 2 * u + (w ^ g.phase);
+}
+// A value for each stream in registers (an indexed array would be memory, on the issuer's path).
+struct Pair {
+  int a, b;
+  __device__ __forceinline__ int operator[](int w) const { return w ? b : a; }
+  __device__ __forceinline__ void add(int w, int x) {
+    a += w ? 0 : x;
+    b += w ? x : 0;
+  }
+};
 
 // Weights of one row's step: P = 2^(s c - m) as bf16 pairs, returning their sum (before the
 // rounding). kPoly of every 8 pairs go to the FMA pipe, the others to the MUFU, spread through the
@@ -263,12 +279,14 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tmap_q);
       walk_to_item(p, walk);
-      int slot = 0, used[2] = {0, 0}, put = 0;
+      int slot = 0, used[2] = {0, 0}, put = 0, phase = 0;
       bool ok = true, more = true;
       for (int sg = 0; ok; ++sg) {
         while (ok && more && put <= sg + kAhead) {
           Segment g{};
           more = next_segment(p, walk, g);     // the last one handed out has no key tiles
+          g.phase = phase;
+          if (!g.two) phase ^= (g.k1 - g.k0) & 1;
           ok = ring_put(bar.ring, put++, g, abort, p.err);
         }
         if (!ok) break;
@@ -299,8 +317,8 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     const uint64_t k_desc = sw128_desc(smem_u32(kv_s), 16, C::kHalves * 1024);
     const uint64_t v_desc = sw128_desc(smem_u32(kv_s), 1024, C::kHalves * 1024);
     const bool leader = elect_one();           // the warp waits, one lane issues
-    int e0 = 0, slot = 0, used[2] = {0, 0};    // first ring entry of the segment, next query slot
-    int done[2] = {0, 0}, segs[2] = {0, 0};    // steps and segments of each stream
+    int e0 = 0, slot = 0;                      // first ring entry of the segment, next query slot
+    Pair used{0, 0}, done{0, 0}, segs{0, 0};   // uses of the slots; steps and segments of the streams
     bool ok = true;
     for (int sg = 0;; ++sg) {
       Segment g;
@@ -308,20 +326,18 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       if (!ok || g.nk == 0) break;
       const bool two = g.two;
       const int n = g.k1 - g.k0;
-      const int steps[2] = {stream_steps(two, 0, n), stream_steps(two, 1, n)};
-      const int qs[2] = {slot, two ? slot ^ 1 : slot};
+      const Pair qs{slot, two ? slot ^ 1 : slot};
       ok = mbar_wait_bounded(&bar.q_full[slot], used[slot] & 1, abort, p.err);
       if (two) ok = ok && mbar_wait_bounded(&bar.q_full[slot ^ 1], used[slot ^ 1] & 1, abort, p.err);
       ok = __all_sync(0xffffffffu, ok);
-      ++used[slot];
-      if (two) ++used[slot ^ 1];
+      used.add(slot, 1);
+      if (two) used.add(slot ^ 1, 1);
       else slot ^= 1;
-      // Stream w's step u takes key tile two ? u : 2 u + w. Stream 1 comes after stream 0: its product
-      // frees a tile that both use, and finds it waited for.
-      auto stage = [&](int w, int u, int kv) { return (e0 + 2 * (two ? u : 2 * u + w) + kv) % C::kStages; };
+      // Stream 1 comes after stream 0: its product frees a tile that both use, and finds it waited for.
+      auto stage = [&](int w, int u, int kv) { return (e0 + 2 * stream_tile(g, w, u) + kv) % C::kStages; };
       auto landed = [&](int w, int u, int kv) {
         if (two && w == 1) return true;
-        const int e = e0 + 2 * (two ? u : 2 * u + w) + kv;
+        const int e = e0 + 2 * stream_tile(g, w, u) + kv;
         return mbar_wait_bounded(&bar.full[e % C::kStages], (e / C::kStages) & 1, abort, p.err);
       };
       auto weighed = [&](int w, int u) {       // P of step u stands, and O may be written
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         mma_commit(&bar.s_full[w]);
         if (w == 1 || !two) mma_commit(&bar.empty[st]);
         // the last product that reads these queries
-        if (two ? u + 1 == steps[w] : 2 * u + w + 1 == n) mma_commit(&bar.q_empty[qs[w]]);
+        if (two ? u + 1 == n : stream_tile(g, w, u) + 1 == n) mma_commit(&bar.q_empty[qs[w]]);
       };
       auto add_v = [&](int w, int u) {         // O += P V
         const uint64_t vd = v_desc + (stage(w, u, 1) * C::kTileBytes >> 4);
@@ -348,18 +364,20 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           for (int c = 0; c < C::kCols / 16; ++c)
             mma_ts(tmem + 256 + (w * C::kSub + j) * D, tmem + w * 128 + j * 64 + c * 8,
                    vd + ((j * C::kCols + c * 16) * (D * 2) >> 4), idesc_o, u > 0 || c > 0 ? 1u : 0u);
-        if (u + 1 == steps[w]) mma_commit(&bar.o_full[w]);
+        if (u + 1 == stream_steps(g, w)) mma_commit(&bar.o_full[w]);
       };
       auto free_v = [&](int w, int u) {
         if (w == 1 || !two) mma_commit(&bar.empty[stage(w, u, 1)]);
       };
-      for (int w = 0; w < 2 && ok; ++w)
-        if (steps[w] > 0) {
+      for (int i = 0; i < 2 && ok; ++i) {
+        const int w = two ? i : i ^ g.phase;   // in the order of their tiles
+        if (stream_steps(g, w) > 0) {
           ok = __all_sync(0xffffffffu, landed(w, 0, 0));
           tc_fence_after();
           if (ok && leader) score(w, 0);
           __syncwarp();
         }
+      }
       if (C::kSub == 2 && two) {
         // products of 64 columns take no longer than their issue: P V of a step and the next S go out
         // back to back, behind all of their waits (with a wait between them 627 for 676 TFLOP/s)
@@ -380,15 +398,16 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         }
       } else {
         // S of the next step as soon as its keys are there
-        for (int u = 0; u < steps[0] && ok; ++u)
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (u >= steps[w]) continue;
+        for (int u = 0; u < (n + 1) >> (two ? 0 : 1) && ok; ++u)
+          for (int i = 0; i < 2 && ok; ++i) {
+            const int w = two ? i : i ^ g.phase;
+            if (u >= stream_steps(g, w)) continue;
             ok = __all_sync(0xffffffffu, landed(w, u, 1) && weighed(w, u));
             if (!ok) break;
             tc_fence_after();
             if (leader) add_v(w, u);
             __syncwarp();
-            if (u + 1 < steps[w]) {
+            if (u + 1 < stream_steps(g, w)) {
               ok = __all_sync(0xffffffffu, landed(w, u + 1, 0));
               if (!ok) break;
               if (leader) score(w, u + 1);
@@ -399,8 +418,8 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           }
       }
       for (int w = 0; w < 2; ++w) {
-        done[w] += steps[w];
-        segs[w] += steps[w] > 0;
+        done.add(w, stream_steps(g, w));
+        segs.add(w, stream_steps(g, w) > 0);
       }
       e0 += 2 * n;
     }
@@ -417,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     const uint32_t s_col = tmem + lane_base + w * 128 + j * 64;
     const uint32_t o_col = tmem + lane_base + 256 + group * D;
     const float c = p.scale_log2;
+    const int r = wq * 32 + lane, r_tok = r / p.G, r_head = r - r_tok * p.G;   // row, its token and head
     int done = 0, segs = 0;
     bool ok = true;
     for (int sg = 0;; ++sg) {
@@ -424,11 +444,10 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
       if (!ok || g.nk == 0) break;
       const bool two = g.two;
-      const int steps = stream_steps(two, w, g.k1 - g.k0);
+      const int steps = stream_steps(g, w);
       const int t0 = g.i * p.item_tokens + (two ? w * p.tile_tokens : 0);
       const int rows = min(p.tile_tokens, g.v.n - t0) * p.G;
-      const int r = wq * 32 + lane;
-      const int tok = t0 + r / p.G;
+      const int tok = t0 + r_tok;
       const bool active = wq * 32 < rows;      // this warp has rows
       // rows of nobody compute what nobody reads: they mask nothing and move nothing
       const int limit = r < rows ? key_limit(p, g.b, g.v, tok) : 1 << 30;
@@ -443,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < C::kCols / 32; ++q)
             tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-          const KeyTile kt = key_tile_at(p, g, g.k0 + (two ? u : 2 * u + w));
+          const KeyTile kt = key_tile_at(p, g, g.k0 + stream_tile(g, w, u));
           const int valid = (kt.b == g.b ? limit : kt.len) - kt.key0 - j * C::kCols;
           const bool masked = __any_sync(0xffffffffu, valid < C::kCols);
           tmem_ld_wait();
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       }
       if (!ok) break;
       done += steps;
-      const int hq = g.h * p.G + r % p.G;
+      const int hq = g.h * p.G + r_head;
       const bool whole = g.k0 == 0 && g.k1 == g.nk && two && writes_rows(p, g.v, g.i);
       const long long out = static_cast<long long>(g.v.r0 + tok) * p.Hq + hq;
       const long long slot = g.k0 == 0 ? row_slot(p, g.b, two ? 0 : w, g.v.r0 + tok, hq)
@@ -523,8 +542,28 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         if (!whole) p.part_ml[slot] = make_float2(m, l);
         else if (p.lse) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
       }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // 32 columns of the row: O or a partial
+      auto store = [&](const uint32_t* o, int q) {
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D + 32 * q);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = pack_bf16(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + 32 * q);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+        }
+      };
       if (active) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -546,23 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
                 o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * own + x.w * other);
               }
             }
-            if (r < rows && whole) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D + 32 * q);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y[i] = pack_bf16(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-                dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            } else if (r < rows) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + 32 * q);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-            }
+            if (r < rows) store(o, q);
           }
           __syncwarp();
         }

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
         Segment g{};                           // the last one handed out has no query tiles
         if (more) {
           const int tiles = (w.v.n + p.tile_tokens - 1) / p.tile_tokens;
-          g = {w.b, w.h, w.kb, w.v, w.t0, w.t1, tiles, tiles > 1 || w.b != last_b || w.h != last_h};
+          g = {w.b, w.h, w.kb, w.v, w.t0, w.t1, tiles, tiles > 1 || w.b != last_b || w.h != last_h, 0};
           last_b = w.b;
           last_h = w.h;
         }
