@@ -474,8 +474,9 @@ typedef struct {
   int32_t num_kv_heads;
   int32_t head_dim;             /* 64 or 128 */
   int32_t page_size;            /* slots per page: 16, 32, 64, 128 or 256 */
-  int32_t max_pages;            /* columns of page_table; a sequence holds max_pages * page_size tokens at most */
-  int32_t prefix_tokens;        /* tokens of the shared prefix; 0: none */
+  int32_t max_pages;            /* columns of page_table; a sequence holds max_pages * page_size (up to 2^29)
+                                   tokens at most */
+  int32_t prefix_tokens;        /* tokens of the shared prefix, up to 2^29; 0: none */
   int64_t pool_pages;           /* pages of each pool; pool_pages * num_kv_heads * page_size < 2^31 */
   void* k_pool;                 /* [pool_pages][num_kv_heads][page_size][head_dim], 16-byte aligned */
   void* v_pool;

@@ -14,7 +14,7 @@ namespace {
 constexpr int kMaxGroup = 64;                  // query heads per KV head
 constexpr int kFewRows = 8;                    // rows a sequence (on average) up to which a CTA appends them
 constexpr int kManyHeads = 8192;               // rows x heads from which on the merge packs four into a warp
-constexpr long long kMaxSlots = 1LL << 30;     // slots of a sequence, tokens of the prefix
+constexpr long long kMaxSlots = 1LL << 29;     // slots of a sequence, tokens of the prefix: their sum is an int
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
 

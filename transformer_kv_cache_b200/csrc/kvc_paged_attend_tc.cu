@@ -440,17 +440,27 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     int done = 0, segs = 0;
     bool ok = true;
     for (int sg = 0;; ++sg) {
-      Segment g;
-      ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
-      if (!ok || g.nk == 0) break;
-      const bool two = g.two;
-      const int steps = stream_steps(g, w);
-      const int t0 = g.i * p.item_tokens + (two ? w * p.tile_tokens : 0);
-      const int rows = min(p.tile_tokens, g.v.n - t0) * p.G;
-      const int tok = t0 + r_tok;
-      const bool active = wq * 32 < rows;      // this warp has rows
-      // rows of nobody compute what nobody reads: they mask nothing and move nothing
-      const int limit = r < rows ? key_limit(p, g.b, g.v, tok) : 1 << 30;
+      // the segment stays in the ring until its end, where it is read again: its fields are not
+      // held in registers through the steps
+      ok = ok && mbar_wait_bounded(&bar.ring.full[sg % kRing], (sg / kRing) & 1, abort, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      int steps, first, stride, limit;         // of the steps' key tiles: the first and their distance; keys seen
+      bool mine, active;                       // this row, this warp has rows
+      {
+        const Segment g = ring_peek(bar.ring, sg);
+        if (g.nk == 0) break;
+        steps = stream_steps(g, w);
+        first = g.k0 + stream_tile(g, w, 0);
+        stride = g.two ? 1 : 2;
+        const int t0 = g.i * p.item_tokens + (g.two ? w * p.tile_tokens : 0);
+        const int rows = min(p.tile_tokens, g.v.n - t0) * p.G;
+        mine = r < rows;
+        active = wq * 32 < rows;
+        // rows of nobody compute what nobody reads: they mask nothing and move nothing. The keys that
+        // the row sees, counted from the segment's tile 0 of its own (a joined prefix comes before).
+        limit = mine ? key_limit(p, g.b, g.v, t0 + r_tok) + prefix_tiles(p) * kTile : 1 << 30;
+      }
       float m = -INFINITY, l = 0.f;
       for (int u = 0; u < steps; ++u) {
         ok = mbar_wait_bounded(&bar.s_full[w], (done + u) & 1, abort, p.err);
@@ -462,8 +472,8 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < C::kCols / 32; ++q)
             tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-          const KeyTile kt = key_tile_at(p, g, g.k0 + stream_tile(g, w, u));
-          const int valid = (kt.b == g.b ? limit : kt.len) - kt.key0 - j * C::kCols;
+          const int tile = first + u * stride;
+          const int valid = (tile < prefix_tiles(p) ? p.prefix_tokens : limit) - tile * kTile - j * C::kCols;
           const bool masked = __any_sync(0xffffffffu, valid < C::kCols);
           tmem_ld_wait();
           if (masked) {
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           }
           // the row's reference maximum moves when a weight would pass 2^8, or on a NaN
           const float mx = row_max(s) * c;
-          const bool move = r < rows && !(mx <= m + kGrow);
+          const bool move = mine && !(mx <= m + kGrow);
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mx : m;
             const float f = move ? ex2(m - m_new) : 1.f;           // 0 from -inf
@@ -507,13 +517,20 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       }
       if (!ok) break;
       done += steps;
-      const int hq = g.h * p.G + r_head;
-      const bool whole = g.k0 == 0 && g.k1 == g.nk && two && writes_rows(p, g.v, g.i);
-      const long long out = static_cast<long long>(g.v.r0 + tok) * p.Hq + hq;
-      const long long slot = g.k0 == 0 ? row_slot(p, g.b, two ? 0 : w, g.v.r0 + tok, hq)
-                                       : cta_slot(p, blockIdx.x, w * kTile + r);
+      bool whole;
+      long long out, slot;                     // the row and head of O, the partial's slot
+      {
+        const Segment g = ring_peek(bar.ring, sg);
+        const int row = g.v.r0 + g.i * p.item_tokens + (g.two ? w * p.tile_tokens : 0) + r_tok;
+        const int hq = g.h * p.G + r_head;
+        whole = g.k0 == 0 && g.k1 == g.nk && g.two && writes_rows(p, g.v, g.i);
+        out = static_cast<long long>(row) * p.Hq + hq;
+        slot = g.k0 == 0 ? row_slot(p, g.b, g.two ? 0 : w, row, hq) : cta_slot(p, blockIdx.x, w * kTile + r);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ring.empty[sg % kRing]);
       if (steps == 0) {
-        if (j == 0 && r < rows) p.part_ml[slot] = make_float2(m, l);
+        if (j == 0 && mine) p.part_ml[slot] = make_float2(m, l);
         continue;
       }
       ok = mbar_wait_bounded(&bar.o_full[w], segs & 1, abort, p.err);
@@ -538,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           m = top;
         }
       }
-      if (j == 0 && r < rows) {
+      if (j == 0 && mine) {
         if (!whole) p.part_ml[slot] = make_float2(m, l);
         else if (p.lse) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
       }
@@ -585,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
                 o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * own + x.w * other);
               }
             }
-            if (r < rows) store(o, q);
+            if (mine) store(o, q);
           }
           __syncwarp();
         }
