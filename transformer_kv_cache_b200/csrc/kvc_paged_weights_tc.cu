@@ -15,18 +15,17 @@
 //
 // Roles: warp 3 walks the schedule and hands out its segments through a ring; warp 0 loads the key
 // tiles by TMA (a page to a copy, looked up one block ahead); warp 2 loads the query tiles and puts
-// their rows' log2-sum-exp and last visible key beside them; warp 1 issues the
-// MMAs (both operands in shared memory); warps 4 and up are the exponentials and sums (thread =
-// key). A warp whose keys every row of the tile sees, which is all but the last tiles of a causal
-// call, adds without looking at the rows' limits (where a row's log2-sum-exp is not finite, nothing
-// is skipped: +inf adds exactly nothing, NaN stays NaN).
+// their rows' log2-sum-exp and last visible key beside them; warp 1 and the last one issue the MMAs
+// of stream 0 and 1 (both operands in shared memory); the warps between are the exponentials and
+// sums (thread = key). A warp whose keys every row of the tile sees, which is all but the last
+// tiles of a causal call, adds without looking at the rows' limits (where a row's log2-sum-exp is
+// not finite, nothing is skipped: +inf adds exactly nothing, NaN stays NaN).
 //
-// Two forms. Where the sequences' rows do not fill a query tile, on average (decode steps), the keys'
-// bytes are the bound: 4 sum warps a stream, most of the shared memory for key tiles (20 warps took 92 for
-// 84 us at 32 sequences of 8,192 tokens). Else the exponentials are: 8 sum warps a stream, four for
-// a query tile's first 64 rows and four for the others (the halves of a key's sum meet in shared
-// memory at the end of a block), so that four warps a scheduler cover one another's waits, an
-// issuing warp for each stream, and as much room for query tiles as for key tiles.
+// Two forms. Where the sequences' rows do not fill a query tile, on average (decode steps), the
+// keys' bytes are the bound: 4 sum warps a stream. Else the exponentials are: 8 sum warps a stream,
+// four for a query tile's first 64 rows and four for the others (the halves of a key's sum meet in
+// shared memory at the end of a block), so that four warps a scheduler cover one another's waits,
+// and as much room for query tiles as for key tiles.
 #include "kvc_paged.cuh"
 #include "kvc_paged_math.cuh"
 
@@ -45,8 +44,7 @@ struct Cfg {
   static constexpr int kKeyStages = (kMany ? 3 : 4) * (D == 128 ? 1 : 2);    // key tiles (two to a block)
   static constexpr int kQueryStages = kMany ? 3 * (D == 128 ? 1 : 2) : 2;
   static constexpr int kSumWarps = kMany ? 16 : 8;
-  static constexpr int kIssuers = kMany ? 2 : 1;           // warp 1, and the last one
-  static constexpr int kThreads = 32 * (4 + kSumWarps + kIssuers - 1);
+  static constexpr int kThreads = 32 * (5 + kSumWarps);    // the last warp issues stream 1's products
   static constexpr int kSmem =
       1024 + (kKeyStages + kQueryStages) * kTileBytes + kQueryStages * kTile * 8 + 2 * kTile * 4 + 1408;
 };
@@ -113,11 +111,11 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kKeyStages; ++i) {
       mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], 1);           // the stream's issuer
+      mbar_init(&bar.k_empty[i], 2);           // both issuers, see there
     }
     for (int i = 0; i < kQueryStages; ++i) {
       mbar_init(&bar.q_full[i], 2);            // the bytes, and the rows' statistics
-      mbar_init(&bar.q_empty[i], C::kIssuers + C::kSumWarps);   // the products, and who reads the statistics
+      mbar_init(&bar.q_empty[i], 2 + C::kSumWarps);   // the products, and who reads the statistics
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.s_full[i >> 1][i & 1], 1);
@@ -277,13 +275,12 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       for (int i = max(0, eq - kQueryStages); i < eq; ++i)
         mbar_wait_drain(&bar.q_full[i % kQueryStages], (i / kQueryStages) & 1, p.err);
   } else if (warp == 1 || warp == 4 + C::kSumWarps) {
-    // ------------------------------------------------------------------ products of streams [w0, w1)
-    const int w0 = warp == 1 ? 0 : 1, w1 = C::kIssuers == 1 ? 2 : w0 + 1;
+    // ------------------------------------------------------------------ products of stream w
+    const int w = warp == 1 ? 0 : 1;
     const uint64_t q_desc = sw128_desc(smem_u32(q_s), 16, 1024);
     const uint64_t k_desc = sw128_desc(smem_u32(k_s), 16, C::kHalves * 1024);
     const bool leader = elect_one();
-    int ek = 0;
-    int steps[2] = {0, 0};
+    int ek = 0, steps = 0;
     QueryWalk q;
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
@@ -305,14 +302,21 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
         const int st = q.eq % kQueryStages;
         const int cols = (tile_rows(p, g, t) + 15) & ~15;
         const uint32_t idesc = idesc_f16kind(1, kTile, 16, 0, 0) + ((static_cast<uint32_t>(cols - 16) >> 3) << 17);
-        ok = __all_sync(0xffffffffu, r);
-        for (int w = w0; w < min(nt, w1) && ok; ++w) {
-          const int ks = (ek + w) % C::kKeyStages, x = steps[w] & 1;
-          if (t == g.k0) r = r && mbar_wait_bounded(&bar.k_full[ks], ((ek + w) / C::kKeyStages) & 1, abort, p.err);
-          if (steps[w] >= 2) r = r && mbar_wait_bounded(&bar.s_empty[w][x], ((steps[w] >> 1) - 1) & 1, abort, p.err);
+        // A tile's stage serves either stream from one round of the ring to the next (a block may have
+        // one tile), and a wait by parity tells a phase only from the one before. So each issuer sees
+        // every tile land, and gives every tile back, the other stream's at once.
+        if (t == g.k0)
+          for (int i = 0; i < nt; ++i) {
+            const int e = ek + i, stage = e % C::kKeyStages;
+            r = r && mbar_wait_bounded(&bar.k_full[stage], (e / C::kKeyStages) & 1, abort, p.err);
+            if (r && i != w && leader) mbar_arrive(&bar.k_empty[stage]);
+          }
+        if (w < nt) {
+          const int ks = (ek + w) % C::kKeyStages, x = steps & 1;
+          if (steps >= 2) r = r && mbar_wait_bounded(&bar.s_empty[w][x], ((steps >> 1) - 1) & 1, abort, p.err);
           ok = __all_sync(0xffffffffu, r);
           if (!ok) break;
-          ++steps[w];
+          ++steps;
           tc_fence_after();
           if (leader) {
             // addresses stay below 2^18: an offset adds to the descriptor's address field
@@ -325,6 +329,8 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
             if (t + 1 == g.k1) mma_commit(&bar.k_empty[ks]);
           }
           __syncwarp();
+        } else {
+          ok = __all_sync(0xffffffffu, r);
         }
         if (!ok) break;
         if (g.nk > 1) {
@@ -336,9 +342,9 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       }
       ek += nt;
     }
-    if (leader) mma_commit(&bar.drained[w0]);
+    if (leader) mma_commit(&bar.drained[w]);
     __syncwarp();
-    mbar_wait_drain(&bar.drained[w0], 0, p.err);
+    mbar_wait_drain(&bar.drained[w], 0, p.err);
   } else {
     // ------------------------------------------------------------------ sums of stream w (rows 64 half ..)
     const int w = kMany ? (warp - 4) >> 3 : (warp - 4) >> 2, half = kMany ? ((warp - 4) >> 2) & 1 : 0, wq = warp & 3;
@@ -358,6 +364,10 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.q_empty[q.eq % kQueryStages]);
         q.held = false;
       }
+      // the score that the sum goes to, asked for now
+      float* score = p.scores + (static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key;
+      const bool adds = half == 0 && g.k0 == 0 && key < g.v.len;
+      const float old = adds ? *score : 0.f;
       float total = 0.f;
       for (int t = g.k0; t < g.k1; ++t) {
         if (g.two) {
@@ -392,10 +402,18 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
             uint32_t s[16];
             tmem_ld16(buf + done, s);
             tmem_ld_wait();
+            if (all) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (done + k < rows && key < limit[done + k])
+              for (int k = 0; k < 16; ++k) {
+                if (done + k >= rows) break;
                 rest += ex2(fmaf(__uint_as_float(s[k]), c, y[done + k]));
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (done + k < rows && key < limit[done + k])
+                  rest += ex2(fmaf(__uint_as_float(s[k]), c, y[done + k]));
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -437,8 +455,8 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       if (g.k0 > 0) {
         p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + at] = total;
         if (warp == 4 && lane == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.i, 1);
-      } else if (key < g.v.len) {
-        p.scores[(static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key] += total;
+      } else if (adds) {
+        *score = old + total;
       }
     }
   }
