@@ -472,6 +472,39 @@ def test_not_a_number_stays_with_its_rows(kvc):
             assert torch.equal(x[keep], y[keep])
 
 
+def test_append_of_rows_far_behind(kvc):
+    """A sequence whose rows stand behind 2^27 others in K and V (32 lanes a row: their number
+    passes 32 bits). The rows before are nobody's, so that they are never touched."""
+    skip, n = (1 << 27) + 5, 9
+    if torch.cuda.mem_get_info()[0] < (skip + n) * 128 + (8 << 30):
+        pytest.skip("needs 26 GB of device memory")
+    t, _ = build(dict(rows=[n], lengths=[20], hq=1, hkv=1, d=64, room=n), "bf16", seed=21)
+    c = copy.deepcopy(t).to(DEV)
+    k = torch.empty(skip + n, 1, 64, dtype=BF16, device=DEV)
+    k[skip:] = c.q
+    kvc.kvc_paged_append(c.handle(kvc), k, k, c.row_start + skip)
+    torch.cuda.synchronize()
+    assert int(c.error) == 0 and c.lengths.tolist() == [20 + n]
+    for slot in range(20, 20 + n):
+        for pool in (c.k_pool, c.v_pool):
+            assert torch.equal(pool[c.page_table[0, slot // 16], 0, slot % 16], c.q[slot - 20, 0])
+
+
+def test_an_infinite_score_is_not_a_number(kvc):
+    """One key with an infinite element: a row with a score of +inf (or 0 x inf) is NaN, as the
+    softmax of the formula is; a row with -inf gives the key a weight of 0. The keys take the
+    places of a tile in turn: exponentials of different places may be computed differently."""
+    for dtype in DTYPES:
+        for d in (64, 128):
+            for key in (0, 13, 127, 128 + 46):
+                t, _ = build(dict(rows=[200], lengths=[400], hq=2, hkv=1, d=d), dtype, seed=20)
+                t.k_pool[t.page_table[0, key // 16], 0, key % 16, 0] = math.inf
+                o, _ = run_attend(kvc, t, False)
+                bad = torch.isnan(o)
+                want = (t.q[:, :, :1] >= 0).expand_as(bad)
+                assert torch.equal(bad, want), (dtype, d, key)
+
+
 def test_no_rows_and_no_lse(kvc):
     t, causal = build("decode, groups of 4", "bf16", seed=19)
     want = run_attend(kvc, t, causal)

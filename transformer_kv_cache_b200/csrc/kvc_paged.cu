@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(512) paged_append_few_kernel(const AppendParam
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, behind = (1 << p.page_shift) - 1;
+  const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), behind = (1 << p.page_shift) - 1;
   const int z = warp - p.rows;
   const int b = z < 0 ? find_sequence(p.row_start, p.B, warp) : z / behind;
   if (b < 0 || b >= p.B) return;                       // behind the last sequence
