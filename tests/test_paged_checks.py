@@ -185,3 +185,16 @@ def test_binding_refuses_host_buffers_and_wrong_tensors():
     for bad in (x[:, :3], x[:, :, :32], x.transpose(0, 1), fused[:, ::3], x[0]):
         with pytest.raises(ValueError):
             kvc._paged_rows(batch, "q", bad, 4)
+
+
+def test_binding_refuses_numbers_past_32_bits():
+    """ctypes would keep their lower 32 bits: 2^32 + 64 tokens to keep would be 64."""
+    import transformer_kv_cache_b200 as kvc
+    for bad in (2 ** 31, 2 ** 32 + 64, -2 ** 31 - 1):
+        for name in ("keep", "sinks", "recent"):
+            with pytest.raises(ValueError, match=name):
+                kvc.kvc_paged_evict(None, **{**dict(keep=64, sinks=4, recent=16), name: bad}, workspace=None)
+        for name in ("rows", "keep"):
+            with pytest.raises(ValueError, match=name):
+                kvc.kvc_paged_workspace(None, **{**dict(rows=5, keep=64), name: bad})
+    kvc._int32(a=-2 ** 31, b=2 ** 31 - 1)

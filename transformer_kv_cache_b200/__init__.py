@@ -441,6 +441,13 @@ def _packed(what, x, device, dtype, shape):
     return x.data_ptr()
 
 
+def _int32(**numbers):
+    """Refuse what ctypes would cut to 32 bits without a word."""
+    for name, x in numbers.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} = {x} does not fit 32 bits")
+
+
 def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, softmax_scale: float, *,
                      prefix_pages=None, prefix_tokens: int = 0, next_positions=None, scores=None, positions=None,
                      error=None) -> kvc_paged_batch:
@@ -460,6 +467,7 @@ def make_paged_batch(k_pool, v_pool, page_table, lengths, num_q_heads: int, soft
     pool_pages, heads, page, dim = k_pool.shape
     slots = (n, heads, max_pages * page)
     b = kvc_paged_batch()
+    _int32(num_q_heads=num_q_heads, prefix_tokens=prefix_tokens)
     b.dtype, b.num_seqs, b.num_q_heads, b.num_kv_heads = types[k_pool.dtype], n, num_q_heads, heads
     b.head_dim, b.page_size, b.max_pages, b.prefix_tokens = dim, page, max_pages, prefix_tokens
     b.pool_pages, b.softmax_scale = pool_pages, softmax_scale
@@ -524,6 +532,7 @@ def _workspace(batch, x):
 
 def kvc_paged_workspace(batch: kvc_paged_batch, rows: int, keep: int = 0) -> int:
     """Bytes of workspace for calls with up to `rows` rows and an eviction to `keep`."""
+    _int32(rows=rows, keep=keep)
     n = ctypes.c_int64(0)
     with batch._torch.cuda.device(batch._device):
         st = _lib.kvc_paged_workspace(batch._ref, rows, keep, ctypes.byref(n))
@@ -566,6 +575,7 @@ def kvc_paged_weights(batch: kvc_paged_batch, q, lse, row_start, workspace, caus
 
 def kvc_paged_evict(batch: kvc_paged_batch, keep: int, sinks: int, recent: int, workspace, stream=None) -> None:
     """Cut every sequence to its `keep` tokens: sinks, recent ones, then the highest scores."""
+    _int32(keep=keep, sinks=sinks, recent=recent)
     wp, wn = _workspace(batch, workspace)
     _paged_call(batch, stream, _lib.kvc_paged_evict, keep, sinks, recent, wp, wn)
 

@@ -630,8 +630,13 @@ cudaError_t launch(cudaStream_t s, const PagedParams& p, const CUtensorMap& q, c
   using C = Cfg<D, SUB>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_tc_kernel<D, SUB>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const void* kernel = reinterpret_cast<const void*>(paged_attend_tc_kernel<D, SUB>);
+    // the warps' shares come out of what the block is launched with; a larger sum would wait forever
+    cudaFuncAttributes at;
+    if (const cudaError_t got = cudaFuncGetAttributes(&at, kernel); got != cudaSuccess) return got;
+    if (at.numRegs * C::kThreads < 32 * (4 * C::kRegsLow + C::kSoftWarps * C::kRegsHigh))
+      return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   return e != cudaSuccess ? e
                           : launch_pdl(paged_attend_tc_kernel<D, SUB>, dim3(p.grid), dim3(C::kThreads), C::kSmem, s, q,
