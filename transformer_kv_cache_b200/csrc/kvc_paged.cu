@@ -83,6 +83,7 @@ PagedParams base_params(const kvc_paged_batch* b, int32_t rows, const int32_t* r
   p.scale_log2 = b->softmax_scale * 1.4426950408889634f;
   p.err = b->error;
   p.grid = sms;
+  p.cost_one = p.cost_two = 1;
   return p;
 }
 
@@ -97,8 +98,13 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
     p->tile_tokens = 128 / p->G;
     p->item_tokens = p->prefix_item_tokens = 2 * p->tile_tokens;
     p->key_tile = 128;
+    p->key_shift = 7;
     p->streams = 2;
     p->slot_rows = 256;
+    // a key tile's time with two tiles of queries to its time with one (2.4 to 1.46 us with 128
+    // dims); with one alone where no item has more
+    p->cost_one = p->rows > p->tile_tokens ? 3 : 1;
+    p->cost_two = p->rows > p->tile_tokens ? 5 : 1;
     p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens;
     return;
   }
@@ -110,6 +116,7 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->prefix_item_tokens = (all <= 16 ? 16 : 64) / p->G;
   p->slot_rows = all <= 16 ? 16 : 64;
   p->key_tile = 64;
+  p->key_shift = 6;
   p->streams = 1;
   p->join = p->prefix_tokens > 0 && p->rows >= static_cast<long long>(p->B) * p->item_tokens && few == 64;
   if (p->D == 64) p->grid *= 2;                // CTAs that fit an SM
@@ -120,12 +127,14 @@ void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
   if (b->dtype == KVC_BF16) {
     p->tile_tokens = p->item_tokens = 128 / p->G;
     p->key_tile = p->slot_rows = 256;
+    p->key_shift = 8;
     p->streams = 1;
     return;
   }
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
   p->tile_tokens = p->item_tokens = (per_seq <= 16 ? 16 : 64) / p->G;
   p->key_tile = 64;
+  p->key_shift = 6;
   p->streams = 1;
   p->slot_rows = p->key_tile;
   p->grid *= 2;
@@ -286,12 +295,6 @@ __global__ void paged_grow_kernel(const AppendParams p) {
 // gets O = 0 and LSE = -inf. Rows that their CTA wrote itself are left alone. What the row needs
 // of the batch is read before the wait for the attention kernel (which had waited for whatever
 // wrote it), the partials after it.
-// x / y in 32 bits where they hold both.
-__device__ __forceinline__ int quotient(long long x, long long y) {
-  if (x >> 32 == 0) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(min(y, 0xffffffffLL)));
-  return static_cast<int>(x / y);
-}
-
 template <typename T, int D, int LANES>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   constexpr int kPer = D / LANES;                      // dims of a lane, as vectors of kVec
@@ -310,9 +313,10 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     const int t = row - v.r0;
     if (t < 0 || t >= v.n) return;
     const int it = item_tokens(p, s), item = t / it, in = t - item * it;
-    nk = item_units(p, s, v, item);
+    // the item's units but for those of its last key tile behind the first one, which counts
+    nk = item_tiles(p, s, v, item) > 0 ? (item_tiles(p, s, v, item) - 1) * tile_cost(p, v, item) + 1 : 0;
     first = h * head_units(p, s, v) + units_before(p, s, v, item);
-    split = p.streams == 2 && v.n - item * p.item_tokens <= p.tile_tokens;
+    split = p.streams == 2 && !two_tiles(p, v, item);
     tile = p.streams == 2 ? in / p.tile_tokens : 0;
     at = (in - tile * p.tile_tokens) * p.G + g;
     whole = writes_rows(p, v, item);
@@ -329,13 +333,13 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   int c0 = 0, c1 = 0, n0 = 0, n1 = 0;
   bool mine = hq < p.Hq;
   if (nk0 > 0) {
-    c0 = quotient(first0, U);
-    n0 = (quotient(first0 + nk0 - 1, U) - c0 + 1) * (split0 ? 2 : 1);
+    c0 = static_cast<int>(quotient(first0, U));
+    n0 = (static_cast<int>(quotient(first0 + nk0 - 1, U)) - c0 + 1) * (split0 ? 2 : 1);
   }
   if (nk1 > 0) {
     const long long u0 = own + first1;
-    c1 = quotient(u0, U);
-    const int pieces = quotient(u0 + nk1 - 1, U) - c1 + 1;
+    c1 = static_cast<int>(quotient(u0, U));
+    const int pieces = static_cast<int>(quotient(u0 + nk1 - 1, U)) - c1 + 1;
     if (pieces == 1 && whole) mine = false;            // written by its CTA
     n1 = pieces * (split1 ? 2 : 1);
   }

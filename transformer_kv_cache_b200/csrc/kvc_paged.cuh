@@ -4,8 +4,9 @@
 // Schedule. The work of a call is a sequence of units; CTA c of the grid takes the units
 // [c * U, (c + 1) * U) with U = ceil(units / CTAs), whatever the lengths on the device are, so
 // a long sequence is split over CTAs and short ones share one, and no host copy of a length is
-// needed (a captured graph follows the lengths of its replay). A unit of attention is one key
-// tile of one item; an item is one KV head with up to item_tokens query tokens of one
+// needed (a captured graph follows the lengths of its replay). A key tile of an attention item is
+// cost_one or cost_two units (and U no less), and belongs to the CTA that has its first one; an
+// item is one KV head with up to item_tokens query tokens of one
 // sequence (its G query heads each), or, for the shared prefix, of the whole batch: there the
 // queries of all sequences are packed, so the prefix is read once for the batch and not once
 // per sequence. The prefix is sequence -1 of the schedule. An item whose units fall into several
@@ -48,9 +49,10 @@ struct PagedParams {
   int item_tokens;              // query tokens of an item
   int prefix_item_tokens;       // the same for the prefix's items
   int tile_tokens;              // query tokens of a tile (the item's, or half of them)
-  int key_tile;                 // keys of a unit
+  int key_tile, key_shift;      // keys of a unit, 1 << key_shift
   int prefix_units;             // key tiles of the prefix
   int streams;                  // tiles of an item: 1, or 2 (an item of one tile splits its keys in two streams)
+  int cost_one, cost_two;       // units of a key tile with one tile of queries, and with two
   int slot_rows;                // rows of a CTA's partial slot
   int grid;                     // CTAs of the schedule
   // workspace
@@ -67,6 +69,11 @@ struct SeqView {
 
 __device__ __forceinline__ int paged_cap(const PagedParams& p) { return p.max_pages << p.page_shift; }
 
+// x / y (neither negative) in 32 bits where they hold both.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if ((x | y) >> 32 == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
 // Sequence b (-1: the prefix and the whole batch's rows), clamped into the tensors.
 __device__ __forceinline__ SeqView seq_view(const PagedParams& p, int b) {
   SeqView v;
@@ -96,9 +103,16 @@ __device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return p.joi
 __device__ __forceinline__ int keys_before(const PagedParams& p, int b, const SeqView& v, int t) {
   return b >= 0 && p.causal ? min(v.len, max(0, v.len - v.n + t)) : v.len;
 }
-__device__ __forceinline__ int item_units(const PagedParams& p, int b, const SeqView& v, int i) {
+// Key tiles of item i, and the units of each.
+__device__ __forceinline__ int item_tiles(const PagedParams& p, int b, const SeqView& v, int i) {
   const int t = min(v.n, (i + 1) * item_tokens(p, b));
-  return prefix_tiles(p) + (keys_before(p, b, v, t) + p.key_tile - 1) / p.key_tile;
+  return prefix_tiles(p) + ((keys_before(p, b, v, t) + p.key_tile - 1) >> p.key_shift);
+}
+__device__ __forceinline__ bool two_tiles(const PagedParams& p, const SeqView& v, int i) {
+  return p.streams == 2 && v.n - i * p.item_tokens > p.tile_tokens;
+}
+__device__ __forceinline__ int tile_cost(const PagedParams& p, const SeqView& v, int i) {
+  return two_tiles(p, v, i) ? p.cost_two : p.cost_one;
 }
 // sum over j < n of floor((a j + b) / m), for a, b >= 0: whole multiples of m come out in closed
 // form, and the rest counts lattice points under a line, which is the same sum with a and m
@@ -106,6 +120,7 @@ __device__ __forceinline__ int item_units(const PagedParams& p, int b, const Seq
 // Every value stays below 2^32: rows and keys of a sequence do.
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long s = 0;
+#pragma unroll 1
   for (;;) {
     s += static_cast<long long>(a / m) * (static_cast<long long>(n) * (n - 1) / 2) +
          static_cast<long long>(b / m) * n;
@@ -123,14 +138,21 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 // Units of a sequence's items [0, i) for one head.
 __device__ __forceinline__ long long units_before(const PagedParams& p, int b, const SeqView& v, int i) {
   if (i <= 0) return 0;
-  if (b < 0 || !p.causal) return static_cast<long long>(i) * item_units(p, b, v, 0);
-  // items before the last see len - n + (j + 1) item_tokens keys, none while that is negative
-  const int whole = min(i, seq_items(p, b, v) - 1);
-  const int it = p.item_tokens, first = v.len - v.n;
-  const int skip = first < 0 ? min(whole, -first / it) : 0;
-  long long s = static_cast<long long>(i) * prefix_tiles(p);
-  if (whole > skip) s += floor_sum(whole - skip, p.key_tile, it, first + (skip + 1) * it + p.key_tile - 1);
-  if (i > whole) s += (v.len + p.key_tile - 1) / p.key_tile;
+  // items before the last are full
+  const int last = seq_items(p, b, v) - 1, whole = min(i, last);
+  const int full = p.streams == 2 ? p.cost_two : p.cost_one;
+  long long s;
+  if (b < 0 || !p.causal) {
+    s = static_cast<long long>(whole) * item_tiles(p, b, v, 0) * full;
+  } else {
+    // they see len - n + (j + 1) item_tokens keys, none while that is negative
+    const int it = p.item_tokens, first = v.len - v.n;
+    const int skip = first < 0 ? min(whole, -first / it) : 0;
+    s = static_cast<long long>(whole) * prefix_tiles(p);
+    if (whole > skip) s += floor_sum(whole - skip, p.key_tile, it, first + (skip + 1) * it + p.key_tile - 1);
+    s *= full;
+  }
+  if (i > whole) s += static_cast<long long>(item_tiles(p, b, v, last)) * tile_cost(p, v, last);
   return s;
 }
 __device__ __forceinline__ long long head_units(const PagedParams& p, int b, const SeqView& v) {
@@ -170,8 +192,9 @@ __device__ __forceinline__ void walk_to(const PagedParams& p, Walk& w, int b) {
 
 // Block-wide: the first unit of every sequence, and this CTA's place in them. units_of_head(b,
 // view) gives the units of one head of sequence b. Every thread of the block calls it; s must
-// hold kPlanWords + blockDim.x / 32 long longs. CTA 0 writes the plan.
-constexpr int kPlanWords = 4;
+// hold kPlanWords + blockDim.x / 32 long longs. CTA 0 writes the plan. (The schedule is written for
+// little code, one place for each computation and no unrolling: it runs once, from a cold cache.)
+constexpr int kPlanWords = 5;
 template <typename HeadUnits>
 __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, HeadUnits&& units_of_head) {
   const int nt = blockDim.x, t = threadIdx.x;
@@ -180,54 +203,55 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
   const int n_seq = p.B - b_first;
   const int per = (n_seq + nt - 1) / nt;
   const int b0 = b_first + min(n_seq, t * per), b1 = b_first + min(n_seq, (t + 1) * per);
-  long long mine = 0;
+  long long at = 0, units = 0, U = 0, u0 = 0, u1 = 0;      // at: units before sequence b
   SeqView view{};
-  for (int b = b0; b < b1; ++b) {
-    if (blockIdx.x == 0 && b >= 0) seq_check(p, b);
-    view = seq_view(p, b);
-    mine += p.Hkv * units_of_head(b, view);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s[kPlanWords + warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < warps; ++w) {
-    const long long x = s[kPlanWords + w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  before += incl - mine;
-  const long long U = (total + p.grid - 1) / p.grid;
-  const long long u0 = min(total, U * blockIdx.x), u1 = min(total, u0 + U);
-  if (blockIdx.x == 0) {
-    if (t == 0) p.plan[0] = U;
-    long long at = before;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      if (b >= 0) p.plan[1 + b] = at;
-      at += p.Hkv * units_of_head(b, seq_view(p, b));
+      if (pass == 0 || per > 1) {              // else they are at hand
+        view = seq_view(p, b);
+        units = units_of_head(b, view);
+      }
+      const long long x = p.Hkv * units;
+      if (pass == 1) {
+        if (blockIdx.x == 0 && b >= 0) {
+          seq_check(p, b);
+          p.plan[1 + b] = at;
+        }
+        if (u0 < u1 && u0 >= at && u0 < at + x) {          // this CTA begins here
+          s[0] = at;
+          s[1] = b;
+          s[2] = (static_cast<long long>(view.n) << 32) | static_cast<uint32_t>(view.r0);
+          s[3] = view.len;
+          s[4] = units;
+        }
+      }
+      at += x;
+    }
+    if (pass == 0) {
+      const long long mine = at;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += o;
+      }
+      if (lane == 31) s[kPlanWords + warp] = at;
+      at -= mine;
+      __syncthreads();
+      long long total = 0;
+#pragma unroll 1
+      for (int w = 0; w < warps; ++w) {
+        const long long x = s[kPlanWords + w];
+        if (w < warp) at += x;
+        total += x;
+      }
+      U = max(quotient(total + p.grid - 1, p.grid), static_cast<long long>(p.cost_two));
+      u0 = min(total, U * blockIdx.x);
+      u1 = min(total, u0 + U);
     }
   }
-  // the thread whose sequences hold unit u0 finds the one
-  if (u0 < u1 && u0 >= before && u0 < before + mine) {
-    long long at = before;
-    int b = b0;
-    if (b1 - b0 > 1)                           // else it is the one whose view is at hand
-      for (;; ++b) {
-        view = seq_view(p, b);
-        const long long x = p.Hkv * units_of_head(b, view);
-        if (u0 < at + x) break;
-        at += x;
-      }
-    s[0] = at;
-    s[1] = b;
-    s[2] = (static_cast<long long>(view.n) << 32) | static_cast<uint32_t>(view.r0);
-    s[3] = view.len;
-  }
+  if (blockIdx.x == 0 && t == 0) p.plan[0] = U;
   __syncthreads();
   Walk w{};
   w.u = u0;
@@ -236,9 +260,8 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
     const int b = static_cast<int>(s[1]);
     w.v = {static_cast<int>(s[2]), static_cast<int>(s[2] >> 32), static_cast<int>(s[3])};
     walk_to(p, w, b);
-    const long long uph = units_of_head(b, w.v);
-    w.h = static_cast<int>((u0 - s[0]) / uph);
-    w.item_first = s[0] + w.h * uph;
+    w.h = static_cast<int>(quotient(u0 - s[0], s[4]));
+    w.item_first = s[0] + w.h * s[4];
     w.i = 0;
   }
   return w;
@@ -247,18 +270,30 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
 __device__ __forceinline__ void walk_to_item(const PagedParams& p, Walk& w) {
   if (w.u >= w.u1) return;
   const long long rel = w.u - w.item_first;
+  long long before = 0;
   int lo = 0, hi = w.items;                    // units_before(lo) <= rel < units_before(hi)
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (units_before(p, w.b, w.v, mid) <= rel) lo = mid;
-    else hi = mid;
+    const long long x = units_before(p, w.b, w.v, mid);
+    if (x <= rel) {
+      lo = mid;
+      before = x;
+    } else {
+      hi = mid;
+    }
   }
-  w.item_first += units_before(p, w.b, w.v, lo);
+  w.item_first += before;
   w.i = lo;
 }
 
-// The next piece of one item in the CTA's units (attention: units are key tiles of items).
+// Tiles of an item whose first unit lies in its first n.
+__device__ __forceinline__ int tiles_before(int n, int cost) {
+  return cost == 1 ? n : static_cast<int>(static_cast<uint32_t>(n + cost - 1) / static_cast<uint32_t>(cost));
+}
+// The next piece of one item in the CTA's units (attention).
 __device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segment& g) {
+#pragma unroll 1
   while (w.u < w.u1) {
     if (w.i >= w.items) {
       w.i = 0;
@@ -269,24 +304,65 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, Walk& w, Segm
       }
       continue;
     }
-    const int nk = item_units(p, w.b, w.v, w.i);
-    if (w.u >= w.item_first + nk) {
-      w.item_first += nk;
+    const int nk = item_tiles(p, w.b, w.v, w.i), cost = tile_cost(p, w.v, w.i);
+    // the tiles whose first unit lies in [u, u1)
+    const long long end = w.item_first + nk * cost;
+    if (w.u > end - cost) {
+      w.u = max(w.u, end);
+      w.item_first = end;
       ++w.i;
       continue;
     }
+    const int k0 = tiles_before(static_cast<int>(w.u - w.item_first), cost);
+    const int k1 = tiles_before(static_cast<int>(min(end, w.u1) - w.item_first), cost);
+    if (k1 <= k0) return false;
     g.b = w.b;
     g.h = w.h;
     g.i = w.i;
     g.v = w.v;
-    g.k0 = static_cast<int>(w.u - w.item_first);
-    g.k1 = static_cast<int>(min(static_cast<long long>(nk), w.u1 - w.item_first));
+    g.k0 = k0;
+    g.k1 = k1;
     g.nk = nk;
-    g.two = p.streams == 2 && w.v.n - w.i * p.item_tokens > p.tile_tokens;
-    w.u = w.item_first + g.k1;
+    g.two = two_tiles(p, w.v, w.i);
+    w.u = w.item_first + k1 * cost;
     return true;
   }
   return false;
+}
+
+// Waits for phase `parity` of `bar`, giving up after a limit or as soon as another role of the CTA
+// has: then *abort is set (the kernel's end latches the error, report_abort) and false returned, and the
+// caller leaves its loop. A kernel has some forty of these, so they are kept short: its code is to
+// fit the instruction cache.
+template <bool kDrain>
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (!kDrain && *abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_near(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return wait_on<false>(bar, parity, abort, KVC_WAIT_LIMIT_NS);
+}
+// For something a whole segment away, which may pass the usual limit: a sequence's 2^22 key tiles
+// take some 10 s.
+__device__ __forceinline__ bool wait_segment(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return wait_on<false>(bar, parity, abort, 30 * KVC_WAIT_LIMIT_NS);
+}
+// For a CTA's own work in flight, whoever gave up.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  wait_on<true>(bar, parity, abort, KVC_WAIT_LIMIT_NS);
+}
+// Behind the block's last barrier.
+__device__ __forceinline__ void report_abort(const PagedParams& p, const volatile int* abort) {
+  if (threadIdx.x == 0 && *abort) latch_error(p.err, DERR_TIMEOUT);
 }
 
 // Segments handed from the warp that walks the schedule to the others of its CTA.
@@ -302,9 +378,9 @@ __device__ __forceinline__ void ring_init(SegmentRing& r, int readers) {
   }
 }
 // The k-th segment into the ring (one thread).
-__device__ __forceinline__ bool ring_put(SegmentRing& r, int k, const Segment& g, volatile int* abort, int* err) {
+__device__ __forceinline__ bool ring_put(SegmentRing& r, int k, const Segment& g, volatile int* abort) {
   const int i = k % kRing;
-  if (k >= kRing && !mbar_wait_bounded(&r.empty[i], ((k / kRing) - 1) & 1, abort, err)) return false;
+  if (k >= kRing && !wait_segment(&r.empty[i], ((k / kRing) - 1) & 1, abort)) return false;
   r.a[i] = make_int4(g.b, g.h, g.i, g.two);
   r.b[i] = make_int4(g.v.r0, g.v.n, g.v.len, g.nk);
   r.c[i] = make_int4(g.k0, g.k1, g.phase, 0);
@@ -317,9 +393,9 @@ __device__ __forceinline__ Segment ring_peek(const SegmentRing& r, int k) {
   return {a.x, a.y, a.z, {b.x, b.y, b.z}, c.x, c.y, b.w, a.w != 0, c.z};
 }
 // The k-th segment out of it (a warp; the same answer in every lane).
-__device__ __forceinline__ bool ring_take(SegmentRing& r, int k, Segment& g, volatile int* abort, int* err) {
+__device__ __forceinline__ bool ring_take(SegmentRing& r, int k, Segment& g, volatile int* abort) {
   const int i = k % kRing;
-  const bool ok = mbar_wait_bounded(&r.full[i], (k / kRing) & 1, abort, err);
+  const bool ok = wait_segment(&r.full[i], (k / kRing) & 1, abort);
   if (!__all_sync(0xffffffffu, ok)) return false;
   g = ring_peek(r, k);
   __syncwarp();
@@ -364,7 +440,7 @@ __device__ __forceinline__ long long cta_slot(const PagedParams& p, int cta, int
 // Whether an item's rows are written to O by the CTA that has all of its keys: two tiles (a
 // stream each) or one stream, and no other part.
 __device__ __forceinline__ bool writes_rows(const PagedParams& p, const SeqView& v, int item) {
-  return parts_of(p) == 1 && (p.streams == 1 || v.n - item * p.item_tokens > p.tile_tokens);
+  return parts_of(p) == 1 && (p.streams == 1 || two_tiles(p, v, item));
 }
 
 // Sequence whose rows hold `row` (row_start[b] <= row < row_start[b + 1]), or -1; warp-wide.
@@ -388,7 +464,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* row_start, int B, in
 // Weights: a unit is one key block (key_tile keys of a sequence, one KV head) with one tile of
 // query tokens, tiles running fastest, so that a key block's sums stay in a CTA.
 __device__ __forceinline__ long long weight_head_units(const PagedParams& p, const SeqView& v) {
-  return static_cast<long long>((v.len + p.key_tile - 1) / p.key_tile) *
+  return static_cast<long long>((v.len + p.key_tile - 1) >> p.key_shift) *
          ((v.n + p.tile_tokens - 1) / p.tile_tokens);
 }
 struct WeightSegment {
@@ -397,6 +473,7 @@ struct WeightSegment {
   int t0, t1;                   // query tiles [t0, t1)
 };
 __device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& w, WeightSegment& g) {
+#pragma unroll 1
   while (w.u < w.u1) {
     const long long uph = weight_head_units(p, w.v);
     if (w.u >= w.item_first + uph) {
@@ -413,7 +490,7 @@ __device__ __forceinline__ bool next_weight_segment(const PagedParams& p, Walk& 
     g.b = w.b;
     g.h = w.h;
     g.v = w.v;
-    g.kb = static_cast<int>(rel / tiles);
+    g.kb = static_cast<int>(quotient(rel, tiles));
     g.t0 = static_cast<int>(rel - static_cast<long long>(g.kb) * tiles);
     g.t1 = static_cast<int>(min(static_cast<long long>(tiles), g.t0 + (w.u1 - w.u)));
     w.u += g.t1 - g.t0;

@@ -23,15 +23,16 @@
 // queries by TMA as a 3-D box (dims, heads, tokens), which packs the rows of any group size; warp 0
 // loads K and V by TMA (a page's slots, all dims, to a box: its rows go by eights, the 64-dim
 // halves of eight rows after one another, so that one copy serves a page and rows keep one
-// distance; one ring in the order K0 V0 K1 V1 ..., the next tile's pages looked up one tile ahead,
+// distance; one ring, a tile's V behind the next one's K, the next tile's pages looked up one tile ahead,
 // across segments); warp 1 issues the MMAs (S = Q K^T: both operands in shared memory; O += P V:
 // P in TMEM, V as an MN-major operand), the streams by turns, which keeps one stream's products
 // under the other's softmax (a warp for each let them run in step: 771 for 952 TFLOP/s at D =
 // 128); the warps from 4 on are the softmax (thread = row = TMEM lane).
 //
 // Slots past a sequence's length are never used: boxes past it are loaded from behind the
-// pool's end, which TMA fills with zeros, the last box of V is copied by the loading warp's threads
-// with zeros behind the last token, and those keys' scores are set to -inf whatever K held.
+// pool's end, which TMA fills with zeros, warp 2 clears the last box of V behind the last token
+// (the loading warp copying that box instead held up all loads: XX for YY us at 64 sequences of
+// 1,024 tokens), and those keys' scores are set to -inf whatever K held.
 //
 // Every barrier wait is bounded; a role that gives up sets the error word, and the CTA drains
 // its copies and products, frees its TMEM and returns.
@@ -60,7 +61,7 @@ struct Cfg {
   static constexpr int kRegsLow = SUB == 1 ? 88 : 64, kRegsHigh = SUB == 1 ? 208 : 104;
   static constexpr int kPoly8 = SUB == 1 ? 0 : 2;              // of 8 pairs, the exponentials on the FMA pipe
   static constexpr int kJoinBytes = kSub == 2 ? 2 * kTile * (D * 4 + 8) : 0;
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kJoinBytes + 1152;
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kJoinBytes + 1216;
 };
 
 struct Bars {
@@ -69,6 +70,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2];
   uint64_t o_full[2], o_free[2];
   uint64_t x_full[2], x_empty[2];              // the second warpgroup's results in shared memory
+  uint64_t tail_full[10];                      // tiles of V that end inside a box, before full
   uint64_t drained;
   SegmentRing ring;
   uint32_t tmem;
@@ -85,6 +87,9 @@ __device__ __forceinline__ int stream_steps(const Segment& g, int w) {
 __device__ __forceinline__ int stream_tile(const Segment& g, int w, int u) {
   return g.two ? u : 2 * u + (w ^ g.phase);
 }
+// The ring holds the tiles of a segment of n in the order in which the streams use them: K0, K1 V0,
+// K2 V1, ..., V(n-1). The entry of V(t):
+__device__ __forceinline__ int v_entry(int t, int n) { return t + 1 == n ? 2 * n - 1 : 2 * t + 2; }
 // A value for each stream in registers (an indexed array would be memory, on the issuer's path).
 struct Pair {
   int a, b;
@@ -131,6 +136,9 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {
   return max3_nan(max3_nan(a[0], a[1], a[2]), max3_nan(a[3], a[4], a[5]), max_nan(a[6], a[7]));
 }
 
+// Whether a tile with `valid` keys before the sequence's end has its last inside a box of blk slots.
+__device__ __forceinline__ bool ends_inside(int valid, int blk) { return valid < kTile && (valid & (blk - 1)); }
+
 template <int D, int SUB>
 __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -143,7 +151,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
   float4* join_o = reinterpret_cast<float4*>(kv_s + C::kStages * C::kTileBytes);    // [stream][4 dims][128 rows]
   float2* join_ml = reinterpret_cast<float2*>(join_o + (C::kSub == 2 ? 2 * kTile * D / 4 : 0));   // [stream][128 rows]
   Bars& bar = *reinterpret_cast<Bars*>(join_ml + (C::kSub == 2 ? 2 * kTile : 0));
-  static_assert(sizeof(Bars) <= 1152, "barriers");
+  static_assert(sizeof(Bars) <= 1216, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bar.abort;
 
@@ -151,6 +159,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.tail_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       mbar_init(&bar.x_empty[i], 4);
     }
     mbar_init(&bar.drained, 1);
-    ring_init(bar.ring, 2 + C::kSoftWarps);    // warps 0, 1 and the softmax
+    ring_init(bar.ring, 3 + C::kSoftWarps);    // warps 0, 1, 2 and the softmax
     bar.abort = 0;
     mbar_fence_init();
   }
@@ -207,72 +216,63 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
                        (key >> p.page_shift));
       return b;
     };
-    // The last box of a sequence's V ends inside: what the cache holds behind the length must not
-    // meet a weight of 0 (0 x NaN), so its rows are copied here, zeros after the last, as the
-    // 128-byte swizzle places them.
-    auto copy_last = [&](uint8_t* dst, int row, int first, int rows) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v_pool) +
-                                                        static_cast<long long>(row) * D);
-      constexpr int kChunks = D / 8;
-#pragma unroll 4
-      for (int i = lane; i < blk * kChunks; i += 32) {
-        const int r = i / kChunks, c = i % kChunks, at = first + r;
-        const uint4 x = row < past && r < rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + ((at >> 3) * C::kHalves + (c >> 3)) * 1024 + (at & 7) * 128 +
-                                  (((c & 7) ^ (at & 7)) << 4)) = x;
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-    };
     int e = 0, sg = 0;
-    bool ok = ring_take(bar.ring, sg++, g, abort, p.err), more = ok && g.nk > 0;
+    bool ok = ring_take(bar.ring, sg++, g, abort), more = ok && g.nk > 0;
     int kt = g.k0;
     Box next = more ? box_at(kt) : Box{-1, 0, 0, 0};
+    int row = past, valid = 0;                 // of the tile before: its V comes behind the next K
+    int st = 0;                                // the next ring entry's stage
+    auto load = [&](const CUtensorMap& map, uint64_t* landed, int from) {
+      ok = ok && (e < C::kStages || wait_near(&bar.empty[st], ((e / C::kStages) - 1) & 1, abort));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      int rows[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows[i] = __shfl_sync(0xffffffffu, from, i) >> 3;
+      if (leader) {
+        uint8_t* dst = kv_s + st * C::kTileBytes;
+        mbar_arrive_expect_tx(landed, C::kTileBytes);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < blocks) tma_load_4d(dst + i * blk * (D * 2), &map, landed, 0, 0, 0, rows[i]);
+      }
+      __syncwarp();
+      ++e;
+      st = st + 1 == C::kStages ? 0 : st + 1;
+    };
+    bool first = true;                         // of its segment
+#pragma unroll 1
     while (ok && more) {
       const Box box = next;
+      bool last = false;
       if (++kt >= g.k1) {
-        ok = ring_take(bar.ring, sg++, g, abort, p.err);
+        last = true;
+        ok = ring_take(bar.ring, sg++, g, abort);
         if (!ok) break;
         more = g.nk > 0;
         kt = g.k0;
       }
       if (more) next = box_at(kt);
       // pool row of this lane's box; behind the pool's end where there is no page (zeros)
-      int row = past;
+      int here = past;
       if (lane < blocks && lane * blk < box.valid) {
         if (box.page < 0 || box.page >= p.pool_pages) latch_error(p.err, DERR_BOUNDS);
-        else row = ((box.page * p.Hkv + box.h) << p.page_shift) + (box.key & ((1 << p.page_shift) - 1));
+        else here = ((box.page * p.Hkv + box.h) << p.page_shift) + (box.key & ((1 << p.page_shift) - 1));
       }
-      int rows[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) rows[i] = __shfl_sync(0xffffffffu, row, i);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int st = e % C::kStages;
-        ok = e < C::kStages || mbar_wait_bounded(&bar.empty[st], ((e / C::kStages) - 1) & 1, abort, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t* dst = kv_s + st * C::kTileBytes;
-        int last = 8;                          // the box that is copied by hand
-        if (kv == 1 && box.valid < kTile && (box.valid & (blk - 1))) {
-          last = box.valid / blk;
-          copy_last(dst, __shfl_sync(0xffffffffu, row, last), last * blk, box.valid & (blk - 1));
-        }
-        if (leader) {
-          mbar_arrive_expect_tx(&bar.full[st], C::kTileBytes - (last < 8 ? C::kHalves * blk * 128 : 0));
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < blocks && i != last)
-              tma_load_4d(dst + i * blk * (D * 2), kv ? &tmap_v : &tmap_k, &bar.full[st], 0, 0, 0, rows[i] >> 3);
-        }
-        __syncwarp();
-        ++e;
-      }
+      load(tmap_k, &bar.full[st], here);
+      // the V of the tile before, and this one's where no other comes
+#pragma unroll 1
+      for (int j = first ? 1 : 0; j < (last ? 2 : 1); ++j)
+        // a tile of V that ends inside a box goes through warp 2
+        load(tmap_v, ends_inside(j ? box.valid : valid, blk) ? &bar.tail_full[st] : &bar.full[st], j ? here : row);
+      row = here;
+      valid = box.valid;
+      first = last;
     }
     // every copy that was issued has landed before the CTA's shared memory goes
     if (lane == 0)
       for (int i = max(0, e - C::kStages); i < e; ++i)
-        mbar_wait_drain(&bar.full[i % C::kStages], (i / C::kStages) & 1, p.err);
+        wait_drain(&bar.full[i % C::kStages], (i / C::kStages) & 1, abort);
   } else if (warp == 3) {
     reg_dealloc<C::kRegsLow>();
     // ------------------------------------------------------------------ schedule and queries
@@ -281,20 +281,25 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       walk_to_item(p, walk);
       int slot = 0, used[2] = {0, 0}, put = 0, phase = 0;
       bool ok = true, more = true;
+#pragma unroll 1
       for (int sg = 0; ok; ++sg) {
-        while (ok && more && put <= sg + kAhead) {
+        // the first queries go out before the segments behind theirs
+        const int ahead = used[slot] == 0 ? 0 : kAhead;
+#pragma unroll 1
+        while (ok && more && put <= sg + ahead) {
           Segment g{};
           more = next_segment(p, walk, g);     // the last one handed out has no key tiles
           g.phase = phase;
           if (!g.two) phase ^= (g.k1 - g.k0) & 1;
-          ok = ring_put(bar.ring, put++, g, abort, p.err);
+          ok = ring_put(bar.ring, put++, g, abort);
         }
         if (!ok) break;
         const Segment g = ring_peek(bar.ring, sg);
         if (g.nk == 0) break;
         const int tiles = g.two ? 2 : 1;
+#pragma unroll 1
         for (int w = 0; w < tiles && ok; ++w) {
-          ok = used[slot] == 0 || mbar_wait_bounded(&bar.q_empty[slot], (used[slot] - 1) & 1, abort, p.err);
+          ok = used[slot] == 0 || wait_segment(&bar.q_empty[slot], (used[slot] - 1) & 1, abort);
           if (!ok) break;
           mbar_arrive_expect_tx(&bar.q_full[slot], C::kHalves * p.tile_tokens * p.G * 128);
           for (int c = 0; c < C::kHalves; ++c)
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         }
       }
       for (int i = 0; i < 2; ++i)
-        if (used[i]) mbar_wait_drain(&bar.q_full[i], (used[i] - 1) & 1, p.err);
+        if (used[i]) wait_drain(&bar.q_full[i], (used[i] - 1) & 1, abort);
     }
   } else if (warp == 1) {
     reg_dealloc<C::kRegsLow>();
@@ -317,117 +322,164 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     const uint64_t k_desc = sw128_desc(smem_u32(kv_s), 16, C::kHalves * 1024);
     const uint64_t v_desc = sw128_desc(smem_u32(kv_s), 1024, C::kHalves * 1024);
     const bool leader = elect_one();           // the warp waits, one lane issues
-    int e0 = 0, slot = 0;                      // first ring entry of the segment, next query slot
+    int st = 0, slot = 0;                      // the next ring entry's stage, the next query slot
+    uint32_t phase = 0;                        // of that stage
+    auto advance = [&] {
+      if (++st == C::kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    };
     Pair used{0, 0}, done{0, 0}, segs{0, 0};   // uses of the slots; steps and segments of the streams
     bool ok = true;
+    // P of step u of the segment stands, and O may be written
+    auto weighed = [&](int w, int u) {
+      if (u == 0 && segs[w] > 0 && !wait_near(&bar.o_free[w], (segs[w] - 1) & 1, abort)) return false;
+      return wait_near(&bar.p_full[w], (done[w] + u) & 1, abort);
+    };
+    auto score = [&](int w, int q, int stage) {            // S = Q K^T
+      const uint64_t qd = q_desc + (q * C::kTileBytes >> 4), kd = k_desc + (stage * C::kTileBytes >> 4);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(tmem + w * 128, qd + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4),
+               kd + (((c >> 2) * 1024 + (c & 3) * 32) >> 4), idesc_s, c > 0 ? 1u : 0u);
+      mma_commit(&bar.s_full[w]);
+    };
+    auto add_v = [&](int w, int u, int stage) {            // O += P V
+      const uint64_t vd = v_desc + (stage * C::kTileBytes >> 4);
+#pragma unroll
+      for (int j = 0; j < C::kSub; ++j)
+#pragma unroll
+        for (int c = 0; c < C::kCols / 16; ++c)
+          mma_ts(tmem + 256 + (w * C::kSub + j) * D, tmem + w * 128 + j * 64 + c * 8,
+                 vd + ((j * C::kCols + c * 16) * (D * 2) >> 4), idesc_o, u > 0 || c > 0 ? 1u : 0u);
+    };
+#pragma unroll 1
     for (int sg = 0;; ++sg) {
       Segment g;
-      ok = ok && ring_take(bar.ring, sg, g, abort, p.err);
+      ok = ok && ring_take(bar.ring, sg, g, abort);
       if (!ok || g.nk == 0) break;
       const bool two = g.two;
       const int n = g.k1 - g.k0;
       const Pair qs{slot, two ? slot ^ 1 : slot};
-      ok = mbar_wait_bounded(&bar.q_full[slot], used[slot] & 1, abort, p.err);
-      if (two) ok = ok && mbar_wait_bounded(&bar.q_full[slot ^ 1], used[slot ^ 1] & 1, abort, p.err);
+      ok = wait_near(&bar.q_full[slot], used[slot] & 1, abort);
+      if (two) ok = ok && wait_near(&bar.q_full[slot ^ 1], used[slot ^ 1] & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       used.add(slot, 1);
       if (two) used.add(slot ^ 1, 1);
       else slot ^= 1;
-      // Stream 1 comes after stream 0: its product frees a tile that both use, and finds it waited for.
-      auto stage = [&](int w, int u, int kv) { return (e0 + 2 * stream_tile(g, w, u) + kv) % C::kStages; };
-      auto landed = [&](int w, int u, int kv) {
-        if (two && w == 1) return true;
-        const int e = e0 + 2 * stream_tile(g, w, u) + kv;
-        return mbar_wait_bounded(&bar.full[e % C::kStages], (e / C::kStages) & 1, abort, p.err);
-      };
-      auto weighed = [&](int w, int u) {       // P of step u stands, and O may be written
-        if (u == 0 && segs[w] > 0 && !mbar_wait_bounded(&bar.o_free[w], (segs[w] - 1) & 1, abort, p.err)) return false;
-        return mbar_wait_bounded(&bar.p_full[w], (done[w] + u) & 1, abort, p.err);
-      };
-      auto score = [&](int w, int u) {         // S = Q K^T
-        const int st = stage(w, u, 0);
-        const uint64_t qd = q_desc + (qs[w] * C::kTileBytes >> 4), kd = k_desc + (st * C::kTileBytes >> 4);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          mma_ss(tmem + w * 128, qd + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4),
-                 kd + (((c >> 2) * 1024 + (c & 3) * 32) >> 4), idesc_s, c > 0 ? 1u : 0u);
-        mma_commit(&bar.s_full[w]);
-        if (w == 1 || !two) mma_commit(&bar.empty[st]);
-        // the last product that reads these queries
-        if (two ? u + 1 == n : stream_tile(g, w, u) + 1 == n) mma_commit(&bar.q_empty[qs[w]]);
-      };
-      auto add_v = [&](int w, int u) {         // O += P V
-        const uint64_t vd = v_desc + (stage(w, u, 1) * C::kTileBytes >> 4);
-#pragma unroll
-        for (int j = 0; j < C::kSub; ++j)
-#pragma unroll
-          for (int c = 0; c < C::kCols / 16; ++c)
-            mma_ts(tmem + 256 + (w * C::kSub + j) * D, tmem + w * 128 + j * 64 + c * 8,
-                   vd + ((j * C::kCols + c * 16) * (D * 2) >> 4), idesc_o, u > 0 || c > 0 ? 1u : 0u);
-        if (u + 1 == stream_steps(g, w)) mma_commit(&bar.o_full[w]);
-      };
-      auto free_v = [&](int w, int u) {
-        if (w == 1 || !two) mma_commit(&bar.empty[stage(w, u, 1)]);
-      };
-      for (int i = 0; i < 2 && ok; ++i) {
-        const int w = two ? i : i ^ g.phase;   // in the order of their tiles
-        if (stream_steps(g, w) > 0) {
-          ok = __all_sync(0xffffffffu, landed(w, 0, 0));
-          tc_fence_after();
-          if (ok && leader) score(w, 0);
-          __syncwarp();
-        }
-      }
-      if (C::kSub == 2 && two) {
-        // products of 64 columns take no longer than their issue: P V of a step and the next S go out
-        // back to back, behind all of their waits (with a wait between them 627 for 676 TFLOP/s)
-        for (int u = 0; u < n && ok; ++u) {
+      if (two) {
+        // Step u of both streams: O += P V(u), S of K(u + 1); K comes first in the ring. Both products of
+        // a stream go out back to back behind all of their waits (with 64 columns they take no longer
+        // than their issue: a wait between them 627 for 676 TFLOP/s).
+#pragma unroll 1
+        for (int u = -1; u < n && ok; ++u) {
+          const bool now = u >= 0, more = u + 1 < n;
+          const int sk = st;
+          const uint32_t pk = phase;
+          if (more) advance();
+          const int sv = st;
+          const uint32_t pv = phase;
+          if (now) advance();
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const bool more = u + 1 < n;
-            ok = ok && __all_sync(0xffffffffu, landed(w, u, 1) && (!more || landed(w, u + 1, 0)) && weighed(w, u));
+            bool r = ok;
+            if (w == 0 && more) r = r && wait_near(&bar.full[sk], pk, abort);
+            if (w == 0 && now) r = r && wait_near(&bar.full[sv], pv, abort);
+            if (now) r = r && weighed(w, u);
+            ok = __all_sync(0xffffffffu, r);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
-              add_v(w, u);
-              if (more) score(w, u + 1);
-              free_v(w, u);
+              if (now) add_v(w, u, sv);
+              if (now && !more) mma_commit(&bar.o_full[w]);
+              if (more) score(w, qs[w], sk);
+              if (more && w == 1) mma_commit(&bar.empty[sk]);
+              if (more && u + 2 == n) mma_commit(&bar.q_empty[qs[w]]);
+              if (now && w == 1) mma_commit(&bar.empty[sv]);
             }
             __syncwarp();
           }
         }
       } else {
-        // S of the next step as soon as its keys are there
-        for (int u = 0; u < (n + 1) >> (two ? 0 : 1) && ok; ++u)
-          for (int i = 0; i < 2 && ok; ++i) {
-            const int w = two ? i : i ^ g.phase;
-            if (u >= stream_steps(g, w)) continue;
-            ok = __all_sync(0xffffffffu, landed(w, u, 1) && weighed(w, u));
+        // The streams take the tiles by turns: V(t), then S of K(t + 2) as soon as it is there.
+#pragma unroll 1
+        for (int t = -2; t < n && ok; ++t) {
+          const int w = (t & 1) ^ g.phase, u = t >> 1, sv = st;
+          if (t >= 0) {
+            ok = __all_sync(0xffffffffu, wait_near(&bar.full[st], phase, abort) && weighed(w, u));
             if (!ok) break;
+            advance();
             tc_fence_after();
-            if (leader) add_v(w, u);
-            __syncwarp();
-            if (u + 1 < stream_steps(g, w)) {
-              ok = __all_sync(0xffffffffu, landed(w, u + 1, 0));
-              if (!ok) break;
-              if (leader) score(w, u + 1);
-              __syncwarp();
+            if (leader) {
+              add_v(w, u, sv);
+              if (t + 2 >= n) mma_commit(&bar.o_full[w]);
             }
-            if (leader) free_v(w, u);
             __syncwarp();
           }
+          if (t + 2 < n) {
+            ok = __all_sync(0xffffffffu, wait_near(&bar.full[st], phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              score(w, qs[0], st);
+              mma_commit(&bar.empty[st]);
+              if (t + 3 == n) mma_commit(&bar.q_empty[qs[0]]);
+            }
+            __syncwarp();
+            advance();
+          }
+          if (t >= 0 && leader) mma_commit(&bar.empty[sv]);
+          __syncwarp();
+        }
       }
+#pragma unroll
       for (int w = 0; w < 2; ++w) {
         done.add(w, stream_steps(g, w));
         segs.add(w, stream_steps(g, w) > 0);
       }
-      e0 += 2 * n;
     }
     if (leader) mma_commit(&bar.drained);
     __syncwarp();
-    mbar_wait_drain(&bar.drained, 0, p.err);
+    wait_drain(&bar.drained, 0, abort);
   } else if (warp == 2) {
-    reg_dealloc<C::kRegsLow>();                // gives up registers, nothing else
+    reg_dealloc<C::kRegsLow>();
+    // ------------------------------------------------------------------ the last values of a sequence
+    // What the cache holds behind a length must not meet a weight of 0 (0 x NaN): zeros to V's rows
+    // behind the last token, up to the end of its box, then the tile is handed on.
+    int e0 = 0;
+    uint32_t phases = 0;                       // of the stages' tail_full
+    bool ok = true;
+    for (int sg = 0; ok; ++sg) {
+      Segment g;
+      ok = ring_take(bar.ring, sg, g, abort);
+      if (!ok || g.nk == 0) break;
+      // the prefix's last tile, where the item has it before its own, and the segment's last
+#pragma unroll 1
+      for (int i = 0; i < 2 && ok; ++i) {
+        const int kt = i ? g.k1 - 1 : prefix_tiles(p) - 1;
+        if (!i && (kt < g.k0 || kt >= g.k1 - 1)) continue;
+        const KeyTile tile = key_tile_at(p, g, kt);
+        const int valid = tile.len - tile.key0;
+        if (!ends_inside(valid, blk)) continue;
+        const int st = (e0 + v_entry(kt - g.k0, g.k1 - g.k0)) % C::kStages;
+        ok = __all_sync(0xffffffffu, wait_segment(&bar.tail_full[st], phases >> st & 1, abort));
+        if (!ok) break;
+        phases ^= 1u << st;
+        uint8_t* v = kv_s + st * C::kTileBytes;
+        const int end = (valid | (blk - 1)) + 1;
+#pragma unroll 1
+        for (int k = valid * C::kHalves + (lane >> 3); k < end * C::kHalves; k += 4) {
+          const int at = k / C::kHalves;       // eight lanes for 128 bytes of a row
+          *reinterpret_cast<uint4*>(v + ((at >> 3) * C::kHalves + k % C::kHalves) * 1024 + (at & 7) * 128 +
+                                    (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.full[st]);
+      }
+      e0 += 2 * (g.k1 - g.k0);
+    }
   } else {
     reg_alloc<C::kRegsHigh>();
     // ------------------------------------------------------------------ softmax: stream w, keys j of a tile
@@ -442,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     for (int sg = 0;; ++sg) {
       // the segment stays in the ring until its end, where it is read again: its fields are not
       // held in registers through the steps
-      ok = ok && mbar_wait_bounded(&bar.ring.full[sg % kRing], (sg / kRing) & 1, abort, p.err);
+      ok = ok && wait_near(&bar.ring.full[sg % kRing], (sg / kRing) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       int steps, first, stride, limit;         // of the steps' key tiles: the first and their distance; keys seen
@@ -463,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       for (int u = 0; u < steps; ++u) {
-        ok = mbar_wait_bounded(&bar.s_full[w], (done + u) & 1, abort, p.err);
+        ok = wait_near(&bar.s_full[w], (done + u) & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -506,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           uint32_t pb[32];
 #pragma unroll
           for (int q = 0; q < C::kCols / 64; ++q) {
-            l += masked ? weigh<0>(&s[64 * q], c2, nm2, pb) : weigh<C::kPoly8>(&s[64 * q], c2, nm2, pb);
+            l += C::kPoly8 > 0 && masked ? weigh<0>(&s[64 * q], c2, nm2, pb) : weigh<C::kPoly8>(&s[64 * q], c2, nm2, pb);
             tmem_st32(s_col + 32 * q, pb);
           }
           tmem_st_wait();
@@ -533,11 +585,11 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         if (j == 0 && mine) p.part_ml[slot] = make_float2(m, l);
         continue;
       }
-      ok = mbar_wait_bounded(&bar.o_full[w], segs & 1, abort, p.err);
+      ok = wait_near(&bar.o_full[w], segs & 1, abort);
       // the second warpgroup's results go to the first through shared memory
       if (C::kSub == 2 && j == 1 && segs > 0)
-        ok = ok && mbar_wait_bounded(&bar.x_empty[w], (segs - 1) & 1, abort, p.err);
-      if (C::kSub == 2 && j == 0) ok = ok && mbar_wait_bounded(&bar.x_full[w], segs & 1, abort, p.err);
+        ok = ok && wait_near(&bar.x_empty[w], (segs - 1) & 1, abort);
+      if (C::kSub == 2 && j == 0) ok = ok && wait_near(&bar.x_full[w], segs & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -618,6 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  report_abort(p, abort);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

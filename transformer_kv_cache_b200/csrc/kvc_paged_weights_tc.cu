@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     if (lane == 0) {
       bool ok = true, more = true;
       int last_b = -1, last_h = -1;
+#pragma unroll 1
       for (int put = 0; ok && more; ++put) {
         WeightSegment w{};
         more = next_weight_segment(p, walk, w);
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
           last_b = w.b;
           last_h = w.h;
         }
-        ok = ring_put(bar.ring, put, g, abort, p.err);
+        ok = ring_put(bar.ring, put, g, abort);
       }
     }
   } else if (warp == 0) {
@@ -183,12 +184,12 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       return b;
     };
     Segment g;
-    ok = ring_take(bar.ring, sg++, g, abort, p.err);
+    ok = ring_take(bar.ring, sg++, g, abort);
     bool more = ok && g.nk > 0;
     Box next = more ? box_of(g) : Box{-1, -1, 0, 0};
     while (ok && more) {
       const Box box = next;
-      ok = ring_take(bar.ring, sg++, g, abort, p.err);
+      ok = ring_take(bar.ring, sg++, g, abort);
       if (!ok) break;
       more = g.nk > 0;
       if (more) next = box_of(g);
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       }
       for (int w = 0; w < box.tiles; ++w, ++ek) {
         const int st = ek % C::kKeyStages;
-        ok = ek < C::kKeyStages || mbar_wait_bounded(&bar.k_empty[st], ((ek / C::kKeyStages) - 1) & 1, abort, p.err);
+        ok = ek < C::kKeyStages || wait_segment(&bar.k_empty[st], ((ek / C::kKeyStages) - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         int rows[8];
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     }
     if (lane == 0)
       for (int i = max(0, ek - C::kKeyStages); i < ek; ++i)
-        mbar_wait_drain(&bar.k_full[i % C::kKeyStages], (i / C::kKeyStages) & 1, p.err);
+        wait_drain(&bar.k_full[i % C::kKeyStages], (i / C::kKeyStages) & 1, abort);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ queries and their statistics
     if (lane == 0) tma_prefetch_desc(&tmap_q);
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       ++t;
       while (first || t >= g.k1) {
         first = false;
-        if (!ring_take(bar.ring, sg++, g, abort, p.err) || g.nk == 0) return false;
+        if (!ring_take(bar.ring, sg++, g, abort) || g.nk == 0) return false;
         t = g.two ? g.k0 : g.k1;               // else the tile is there already
       }
       const int rows = tile_rows(p, g, t);
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     while (more) {
       const int st = eq % kQueryStages;
       const int tok0 = t * p.tile_tokens, rows = tile_rows(p, g, t);
-      bool ok = eq < kQueryStages || mbar_wait_bounded(&bar.q_empty[st], ((eq / kQueryStages) - 1) & 1, abort, p.err);
+      bool ok = eq < kQueryStages || wait_segment(&bar.q_empty[st], ((eq / kQueryStages) - 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar.q_full[st], C::kHalves * p.tile_tokens * p.G * 128);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     }
     if (lane == 0)
       for (int i = max(0, eq - kQueryStages); i < eq; ++i)
-        mbar_wait_drain(&bar.q_full[i % kQueryStages], (i / kQueryStages) & 1, p.err);
+        wait_drain(&bar.q_full[i % kQueryStages], (i / kQueryStages) & 1, abort);
   } else if (warp == 1 || warp == 4 + C::kSumWarps) {
     // ------------------------------------------------------------------ products of stream w
     const int w = warp == 1 ? 0 : 1;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       Segment g;
-      ok = ring_take(bar.ring, sg, g, abort, p.err);
+      ok = ring_take(bar.ring, sg, g, abort);
       if (!ok || g.nk == 0) break;
       const int nt = block_tiles(g);
       if (g.two && q.held) {
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
         bool r = true;
         if (g.two) {
           ++q.eq;
-          r = mbar_wait_bounded(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort, p.err);
+          r = wait_near(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort);
         }
         const int st = q.eq % kQueryStages;
         const int cols = (tile_rows(p, g, t) + 15) & ~15;
@@ -308,12 +309,12 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
         if (t == g.k0)
           for (int i = 0; i < nt; ++i) {
             const int e = ek + i, stage = e % C::kKeyStages;
-            r = r && mbar_wait_bounded(&bar.k_full[stage], (e / C::kKeyStages) & 1, abort, p.err);
+            r = r && wait_near(&bar.k_full[stage], (e / C::kKeyStages) & 1, abort);
             if (r && i != w && leader) mbar_arrive(&bar.k_empty[stage]);
           }
         if (w < nt) {
           const int ks = (ek + w) % C::kKeyStages, x = steps & 1;
-          if (steps >= 2) r = r && mbar_wait_bounded(&bar.s_empty[w][x], ((steps >> 1) - 1) & 1, abort, p.err);
+          if (steps >= 2) r = r && wait_near(&bar.s_empty[w][x], ((steps >> 1) - 1) & 1, abort);
           ok = __all_sync(0xffffffffu, r);
           if (!ok) break;
           ++steps;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     }
     if (leader) mma_commit(&bar.drained[w]);
     __syncwarp();
-    mbar_wait_drain(&bar.drained[w], 0, p.err);
+    wait_drain(&bar.drained[w], 0, abort);
   } else {
     // ------------------------------------------------------------------ sums of stream w (rows 64 half ..)
     const int w = kMany ? (warp - 4) >> 3 : (warp - 4) >> 2, half = kMany ? ((warp - 4) >> 2) & 1 : 0, wq = warp & 3;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     bool ok = true;
     for (int sg = 0; ok; ++sg) {
       Segment g;
-      ok = ring_take(bar.ring, sg, g, abort, p.err);
+      ok = ring_take(bar.ring, sg, g, abort);
       if (!ok || g.nk == 0) break;
       const bool mine = w < block_tiles(g);
       const int key0 = g.i * 2 * kTile + w * kTile + wq * 32, key = key0 + lane;
@@ -372,13 +373,13 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       for (int t = g.k0; t < g.k1; ++t) {
         if (g.two) {
           ++q.eq;
-          ok = mbar_wait_bounded(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort, p.err);
+          ok = wait_near(&bar.q_full[q.eq % kQueryStages], (q.eq / kQueryStages) & 1, abort);
         }
         const int st = q.eq % kQueryStages;
         if (mine) {
           const int rows = min(tile_rows(p, g, t), kMany ? 64 * half + 64 : kTile);
           const int x = steps & 1;
-          ok = ok && mbar_wait_bounded(&bar.s_full[w][x], (steps >> 1) & 1, abort, p.err);
+          ok = ok && wait_near(&bar.s_full[w][x], (steps >> 1) & 1, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++steps;
@@ -435,14 +436,14 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
       if (kMany && (g.nk > 1 || tile_rows(p, g, 0) > 64)) {
         // the second rows' sum to the first ones' warp of the same keys
         if (half == 1) {
-          ok = met == 0 || mbar_wait_bounded(&bar.x_empty[w], (met - 1) & 1, abort, p.err);
+          ok = met == 0 || wait_near(&bar.x_empty[w], (met - 1) & 1, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           half_s[at] = total;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.x_full[w]);
         } else {
-          ok = mbar_wait_bounded(&bar.x_full[w], met & 1, abort, p.err);
+          ok = wait_near(&bar.x_full[w], met & 1, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           total += half_s[at];
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  report_abort(p, abort);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
