@@ -90,16 +90,6 @@ __device__ __forceinline__ int stream_tile(const Segment& g, int w, int u) {
 // The ring holds the tiles of a segment of n in the order in which the streams use them: K0, K1 V0,
 // K2 V1, ..., V(n-1). The entry of V(t):
 __device__ __forceinline__ int v_entry(int t, int n) { return t + 1 == n ? 2 * n - 1 : 2 * t + 2; }
-// A value for each stream in registers (an indexed array would be memory, on the issuer's path).
-struct Pair {
-  int a, b;
-  __device__ __forceinline__ int operator[](int w) const { return w ? b : a; }
-  __device__ __forceinline__ void add(int w, int x) {
-    a += w ? 0 : x;
-    b += w ? x : 0;
-  }
-};
-
 // Weights of one row's step: P = 2^(s c - m) as bf16 pairs, returning their sum (before the
 // rounding). kPoly of every 8 pairs go to the FMA pipe, the others to the MUFU, spread through the
 // row. Masked steps hold -inf and use the MUFU alone, which gives exact zeros.
@@ -330,12 +320,13 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         phase ^= 1;
       }
     };
-    Pair used{0, 0}, done{0, 0}, segs{0, 0};   // uses of the slots; steps and segments of the streams
+    // bit w: the phases of the query slots, of the streams' P and of their O
+    uint32_t q_phase = 0, p_phase = 0, o_phase = 0;
     bool ok = true;
     // P of step u of the segment stands, and O may be written
     auto weighed = [&](int w, int u) {
-      if (u == 0 && segs[w] > 0 && !wait_near(&bar.o_free[w], (segs[w] - 1) & 1, abort)) return false;
-      return wait_near(&bar.p_full[w], (done[w] + u) & 1, abort);
+      if (u == 0 && !wait_near(&bar.o_free[w], (o_phase >> w & 1) ^ 1, abort)) return false;   // at once the first time
+      return wait_near(&bar.p_full[w], ((p_phase >> w) + u) & 1, abort);
     };
     auto score = [&](int w, int q, int stage) {            // S = Q K^T
       const uint64_t qd = q_desc + (q * C::kTileBytes >> 4), kd = k_desc + (stage * C::kTileBytes >> 4);
@@ -361,42 +352,57 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       if (!ok || g.nk == 0) break;
       const bool two = g.two;
       const int n = g.k1 - g.k0;
-      const Pair qs{slot, two ? slot ^ 1 : slot};
-      ok = wait_near(&bar.q_full[slot], used[slot] & 1, abort);
-      if (two) ok = ok && wait_near(&bar.q_full[slot ^ 1], used[slot ^ 1] & 1, abort);
+      const int q0 = slot;
+      ok = wait_near(&bar.q_full[q0], q_phase >> q0 & 1, abort);
+      if (two) ok = ok && wait_near(&bar.q_full[q0 ^ 1], q_phase >> (q0 ^ 1) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
-      used.add(slot, 1);
-      if (two) used.add(slot ^ 1, 1);
-      else slot ^= 1;
+      q_phase ^= two ? 3u : 1u << q0;
+      if (!two) slot ^= 1;
       if (two) {
         // Step u of both streams: O += P V(u), S of K(u + 1); K comes first in the ring. Both products of
         // a stream go out back to back behind all of their waits (with 64 columns they take no longer
         // than their issue: a wait between them 627 for 676 TFLOP/s).
+        ok = ok && __all_sync(0xffffffffu, wait_near(&bar.full[st], phase, abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll 1
-        for (int u = -1; u < n && ok; ++u) {
-          const bool now = u >= 0, more = u + 1 < n;
+          for (int w = 0; w < 2; ++w) {
+            score(w, q0 ^ w, st);
+            if (n == 1) mma_commit(&bar.q_empty[q0 ^ w]);
+          }
+          mma_commit(&bar.empty[st]);
+        }
+        __syncwarp();
+        advance();
+#pragma unroll 1
+        for (int u = 0; u < n && ok; ++u) {
+          const bool more = u + 1 < n;
           const int sk = st;
           const uint32_t pk = phase;
           if (more) advance();
           const int sv = st;
           const uint32_t pv = phase;
-          if (now) advance();
+          advance();
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             bool r = ok;
-            if (w == 0 && more) r = r && wait_near(&bar.full[sk], pk, abort);
-            if (w == 0 && now) r = r && wait_near(&bar.full[sv], pv, abort);
-            if (now) r = r && weighed(w, u);
+            if (w == 0)
+              r = r && wait_near(&bar.full[sv], pv, abort) && (!more || wait_near(&bar.full[sk], pk, abort));
+            r = r && weighed(w, u);
             ok = __all_sync(0xffffffffu, r);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
-              if (now) add_v(w, u, sv);
-              if (now && !more) mma_commit(&bar.o_full[w]);
-              if (more) score(w, qs[w], sk);
-              if (more && w == 1) mma_commit(&bar.empty[sk]);
-              if (more && u + 2 == n) mma_commit(&bar.q_empty[qs[w]]);
-              if (now && w == 1) mma_commit(&bar.empty[sv]);
+              add_v(w, u, sv);
+              if (more) {
+                score(w, q0 ^ w, sk);
+                if (w == 1) mma_commit(&bar.empty[sk]);
+                if (u + 2 == n) mma_commit(&bar.q_empty[q0 ^ w]);
+              } else {
+                mma_commit(&bar.o_full[w]);
+              }
+              if (w == 1) mma_commit(&bar.empty[sv]);
             }
             __syncwarp();
           }
@@ -422,9 +428,9 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (leader) {
-              score(w, qs[0], st);
+              score(w, q0, st);
               mma_commit(&bar.empty[st]);
-              if (t + 3 == n) mma_commit(&bar.q_empty[qs[0]]);
+              if (t + 3 == n) mma_commit(&bar.q_empty[q0]);
             }
             __syncwarp();
             advance();
@@ -435,8 +441,9 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        done.add(w, stream_steps(g, w));
-        segs.add(w, stream_steps(g, w) > 0);
+        const int steps = stream_steps(g, w);
+        p_phase ^= static_cast<uint32_t>(steps & 1) << w;
+        o_phase ^= static_cast<uint32_t>(steps > 0) << w;
       }
     }
     if (leader) mma_commit(&bar.drained);
