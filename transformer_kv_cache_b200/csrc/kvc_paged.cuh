@@ -190,18 +190,23 @@ __device__ __forceinline__ void walk_to(const PagedParams& p, Walk& w, int b) {
   if (b + 1 < p.B) w.next = seq_view(p, b + 1);
 }
 
-// Block-wide: the first unit of every sequence, and this CTA's place in them. units_of_head(b,
-// view) gives the units of one head of sequence b. Every thread of the block calls it; s must
-// hold kPlanWords + blockDim.x / 32 long longs. CTA 0 writes the plan. (The schedule is written for
+// The first unit of every sequence, and this CTA's place in them. units_of_head(b, view) gives the
+// units of one head of sequence b. Of 32 sequences any warp finds out by itself (plan_by_warp), and
+// only a warp that needs the walk calls this (a decode step of 4: 15.6 us block-wide, 14.7 so; of 64
+// with two or three to a lane: 70 and 74); else every thread of the block does. s must hold
+// kPlanWords + blockDim.x / 32 long longs. CTA 0 writes the plan. (The schedule is written for
 // little code, one place for each computation and no unrolling: it runs once, from a cold cache.)
 constexpr int kPlanWords = 5;
+__device__ __forceinline__ int first_sequence(const PagedParams& p) { return p.prefix_tokens > 0 && !p.join ? -1 : 0; }
+__device__ __forceinline__ bool plan_by_warp(const PagedParams& p) { return p.B - first_sequence(p) <= 32; }
 template <typename HeadUnits>
 __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, HeadUnits&& units_of_head) {
-  const int nt = blockDim.x, t = threadIdx.x;
-  const int lane = t & 31, warp = t >> 5, warps = nt >> 5;
-  const int b_first = p.prefix_tokens > 0 && !p.join ? -1 : 0;
+  const bool alone = plan_by_warp(p);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int nt = alone ? 32 : blockDim.x, t = alone ? lane : threadIdx.x;
+  const int b_first = first_sequence(p);
   const int n_seq = p.B - b_first;
-  const int per = (n_seq + nt - 1) / nt;
+  const int per = alone ? 1 : (n_seq + nt - 1) / nt;
   const int b0 = b_first + min(n_seq, t * per), b1 = b_first + min(n_seq, (t + 1) * per);
   long long at = 0, units = 0, U = 0, u0 = 0, u1 = 0;      // at: units before sequence b
   SeqView view{};
@@ -236,15 +241,19 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
         const long long o = __shfl_up_sync(0xffffffffu, at, d);
         if (lane >= d) at += o;
       }
-      if (lane == 31) s[kPlanWords + warp] = at;
+      long long total = __shfl_sync(0xffffffffu, at, 31);
       at -= mine;
-      __syncthreads();
-      long long total = 0;
-#pragma unroll 1
-      for (int w = 0; w < warps; ++w) {
-        const long long x = s[kPlanWords + w];
-        if (w < warp) at += x;
-        total += x;
+      if (!alone) {                            // the warps' sums, a lane for each
+        if (lane == 0) s[kPlanWords + warp] = total;
+        __syncthreads();
+        long long x = lane < warps ? s[kPlanWords + lane] : 0, y = lane < warp ? x : 0;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, d);
+          y += __shfl_xor_sync(0xffffffffu, y, d);
+        }
+        total = x;
+        at += y;
       }
       U = max(quotient(total + p.grid - 1, p.grid), static_cast<long long>(p.cost_two));
       u0 = min(total, U * blockIdx.x);
@@ -252,7 +261,9 @@ __device__ __forceinline__ Walk plan_walk(const PagedParams& p, long long* s, He
     }
   }
   if (blockIdx.x == 0 && t == 0) p.plan[0] = U;
-  __syncthreads();
+  // (several warps that are alone write the same)
+  if (alone) __syncwarp();
+  else __syncthreads();
   Walk w{};
   w.u = u0;
   w.u1 = u1;

@@ -170,12 +170,14 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     tmem_alloc(&bar.tmem, 512);
     tmem_relinquish();
   }
-  griddep_wait();                              // everything above is this CTA's own
-  griddep_launch_dependents();
-  Walk walk = plan_walk(p, bar.plan, [&](int b, const SeqView& v) { return head_units(p, b, v); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();                              // everything above is this CTA's own
+  griddep_launch_dependents();
+  Walk walk{};
+  if (warp == 3 || !plan_by_warp(p))
+    walk = plan_walk(p, bar.plan, [&](int b, const SeqView& v) { return head_units(p, b, v); });
   const uint32_t tmem = bar.tmem;
   // TMEM columns: S of stream w at 128 w, the weights of its warpgroup j at 128 w + 64 j, their O at
   // 256 + (w * kSub + j) * D

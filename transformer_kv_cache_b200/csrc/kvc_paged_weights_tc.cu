@@ -134,13 +134,15 @@ __global__ void __launch_bounds__(Cfg<D, kMany>::kThreads, 1)
     tmem_alloc(&bar.tmem, 512);
     tmem_relinquish();
   }
-  griddep_wait();                              // everything above is this CTA's own
-  griddep_launch_dependents();
-  if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
-  Walk walk = plan_walk(p, bar.plan, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();                              // everything above is this CTA's own
+  griddep_launch_dependents();
+  if (threadIdx.x == 4 * 32) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);   // the thread that may write it later
+  Walk walk{};
+  if (warp == 3 || !plan_by_warp(p))
+    walk = plan_walk(p, bar.plan, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   const uint32_t tmem = bar.tmem;              // S^T buffer x of stream w: columns (2 w + x) * 128
 
   if (warp == 3) {
