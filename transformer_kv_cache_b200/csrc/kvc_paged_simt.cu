@@ -19,21 +19,6 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// Keys [key0, key0 + kKT) of one pool into shared memory; keys from `end` on are zeros.
-template <int D, int LD>
-__device__ __forceinline__ void load_keys(const PagedParams& p, const void* pool, int b, int h, int key0, int end,
-                                          float* dst) {
-  constexpr int kChunks = D / 4;
-  for (int i = threadIdx.x; i < kKT * kChunks; i += kThreads) {
-    const int key = i / kChunks, c = i % kChunks;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key0 + key < end) {
-      const long long row = pool_row(p, b, h, key0 + key);
-      if (row >= 0) x = load4(static_cast<const float*>(pool) + row * D + c * 4);
-    }
-    *reinterpret_cast<float4*>(dst + key * LD + c * 4) = x;
-  }
-}
 // The tile's query rows [token t0 .., G heads each]; rows past `tokens` are zeros.
 template <int D, int LD, int ROWS>
 __device__ __forceinline__ void load_queries(const PagedParams& p, const SeqView& v, int h, int t0, int rows,
@@ -80,15 +65,15 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, b
 }
 
 // A CTA's loads of key tiles: a thread copies the same 16 bytes of kKeys of a tile's keys, whose
-// pages it asks for one tile ahead.
+// pages it asks for one tile ahead. Keys that no page holds are zeros.
 template <int D>
 struct KeyLoader {
   static constexpr int kChunks = D / 4, kKeys = kKT * kChunks / kThreads, kStep = kThreads / kChunks;
   int page[kKeys];
   KeyTile tile;
 
-  __device__ __forceinline__ void look(const PagedParams& p, const Segment& g, int kt) {
-    tile = key_tile_at(p, g, kt);
+  __device__ __forceinline__ void look(const PagedParams& p, const KeyTile& t) {
+    tile = t;
     const int32_t* table =
         tile.b < 0 ? p.prefix_pages : p.page_table + static_cast<long long>(tile.b) * p.max_pages;
 #pragma unroll
@@ -97,6 +82,7 @@ struct KeyLoader {
       page[i] = key < tile.len ? __ldg(table + (key >> p.page_shift)) : -1;
     }
   }
+  template <bool kValues>
   __device__ __forceinline__ void load(const PagedParams& p, int h, float* ks, float* vs, int ld) const {
     const int c = static_cast<int>(threadIdx.x) % kChunks;
 #pragma unroll
@@ -108,11 +94,15 @@ struct KeyLoader {
                                         (key & ((1 << p.page_shift) - 1))
                                   : 0;
       cp_async16_or_zero(ks + at * ld + c * 4, static_cast<const float*>(p.k_pool) + row * D + c * 4, there);
-      cp_async16_or_zero(vs + at * ld + c * 4, static_cast<const float*>(p.v_pool) + row * D + c * 4, there);
+      if (kValues) cp_async16_or_zero(vs + at * ld + c * 4, static_cast<const float*>(p.v_pool) + row * D + c * 4, there);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   }
 };
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // One segment in tiles of ROWS query rows; sm holds [rows][LD] queries, two stages of [kKT][LD] keys
 // and values, [rows][LP] weights.
@@ -126,9 +116,10 @@ __device__ __forceinline__ void attend_segment(const PagedParams& p, const Segme
   const int t0 = g.i * item_tokens(p, g.b);
   const int tokens = min(item_tokens(p, g.b), g.v.n - t0), rows = tokens * p.G;
   KeyLoader<D> loader;
-  loader.look(p, g, g.k0);
+  loader.look(p, key_tile_at(p, g, g.k0));
   __syncthreads();                             // the segment before is read
-  loader.load(p, g.h, kv, kv + kKT * LD, LD);
+  loader.template load<true>(p, g.h, kv, kv + kKT * LD, LD);
+  cp_async_commit();
   load_queries<D, LD, ROWS>(p, g.v, g.h, t0, rows, qs);
   float m[RPT], l[RPT], acc[RPT][D / 16];
   int limit[RPT];
@@ -141,18 +132,19 @@ __device__ __forceinline__ void attend_segment(const PagedParams& p, const Segme
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) acc[r][c] = 0.f;
   }
-  if (g.k0 + 1 < g.k1) loader.look(p, g, g.k0 + 1);
+  if (g.k0 + 1 < g.k1) loader.look(p, key_tile_at(p, g, g.k0 + 1));
   for (int kt = g.k0; kt < g.k1; ++kt) {
     const int st = (kt - g.k0) & 1;
     const float* ks = kv + st * 2 * kKT * LD;
     const float* vs = ks + kKT * LD;
     if (kt + 1 < g.k1) {
       float* next = kv + (st ^ 1) * 2 * kKT * LD;
-      loader.load(p, g.h, next, next + kKT * LD, LD);
-      if (kt + 2 < g.k1) loader.look(p, g, kt + 2);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      loader.template load<true>(p, g.h, next, next + kKT * LD, LD);
+      cp_async_commit();
+      if (kt + 2 < g.k1) loader.look(p, key_tile_at(p, g, kt + 2));
+      cp_async_wait<1>();
     } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      cp_async_wait<0>();
     }
     __syncthreads();
     const KeyTile tile = key_tile_at(p, g, kt);
@@ -251,61 +243,146 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
   }
 }
 
+// Weights: a step of a CTA is a block of kKT keys with one tile of ROWS query rows; keys, rows and
+// their log-sum-exp arrive by cp.async kStages - 1 steps ahead, the steps' descriptions beside them.
+template <int D, int ROWS>
+struct WeightsCfg {
+  static constexpr int kLD = D + 4;
+  // as many as leave room for two CTAs of an SM, or one where a step takes 67 KB
+  static constexpr int kStages = D == 64 ? (ROWS == 16 ? 4 : 3) : (ROWS == 16 ? 2 : 3);
+  static constexpr int kFloats = (kKT + ROWS) * kLD + ROWS;
+  static constexpr size_t kSmem = sizeof(float) * kStages * kFloats;
+};
+struct WeightStep {
+  int b, h, kb, t;                             // sequence, KV head, key block, query tile
+  int last, first;                             // 1: the CTA's last of the block; the CTA has the block's first
+  SeqView v;
+};
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const PagedParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int LD = D + 4, RPT = ROWS / 16;
-  extern __shared__ float sm[];
-  float* qs = sm;                              // [ROWS][LD]
-  float* ks = qs + ROWS * LD;                  // [kKT][LD]
+  using C = WeightsCfg<D, ROWS>;
+  constexpr int LD = C::kLD, RPT = ROWS / 16, kStages = C::kStages, kChunks = D / 4;
+  extern __shared__ __align__(16) float sm[];  // [stage][keys | rows][LD], [rows] log-sum-exp
   __shared__ long long plan_s[kPlanWords + kThreads / 32];
+  __shared__ WeightStep steps_s[kStages];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Walk w = plan_walk(p, plan_s, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
-  WeightSegment g;
-  while (next_weight_segment(p, w, g)) {
-    const int key0 = g.kb * kKT;
-    __syncthreads();
-    load_keys<D, LD>(p, p.k_pool, g.b, g.h, key0, g.v.len, ks);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t = g.t0; t < g.t1; ++t) {
-      const int tok0 = t * p.tile_tokens;
-      const int rows = min(p.tile_tokens, g.v.n - tok0) * p.G;
-      __syncthreads();
-      load_queries<D, LD, ROWS>(p, g.v, g.h, tok0, rows, qs);
-      __syncthreads();
-      float s[4][RPT];
-      dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
+  // the step that is looked up; its head's key blocks and query tiles
+  int kb = 0, t = 0, blocks = 0, tiles = 0;
+  bool more = w.u < w.u1, first = false;
+  auto head_size = [&] {
+    blocks = (w.v.len + kKT - 1) / kKT;
+    tiles = (w.v.n + p.tile_tokens - 1) / p.tile_tokens;
+  };
+  KeyLoader<D> loader;
+  if (more) {
+    head_size();
+    kb = static_cast<int>(quotient(w.u - w.item_first, tiles));
+    t = static_cast<int>(w.u - w.item_first - static_cast<long long>(kb) * tiles);
+    first = t == 0;
+    loader.look(p, {w.b, kb * kKT, w.v.len});
+  }
+  // this thread's 16 bytes of a tile's rows: their token and head
+  constexpr int kRows = ROWS * kChunks / kThreads, kStep = kThreads / kChunks;
+  const int c = static_cast<int>(threadIdx.x) % kChunks, r0 = static_cast<int>(threadIdx.x) / kChunks;
+  int tok[kRows], head[kRows];
 #pragma unroll
-      for (int j = 0; j < RPT; ++j) {
-        const int r = tx + 16 * j;
-        if (r < rows) {
-          const int tok = tok0 + r / p.G;
-          const int limit = key_limit(p, g.b, g.v, tok);
-          const float lse2 =
-              p.lse[static_cast<long long>(g.v.r0 + tok) * p.Hq + g.h * p.G + r % p.G] * 1.4426950408889634f;
+  for (int i = 0; i < kRows; ++i) {
+    tok[i] = (r0 + i * kStep) / p.G;
+    head[i] = (r0 + i * kStep) % p.G;
+  }
+  int put = 0;                                 // steps whose loads are out
+  auto issue = [&] {                           // the step's loads, and the look-up of the next one's
+    if (more) {
+      float* ks = sm + put % kStages * C::kFloats;
+      float* qs = ks + kKT * LD + r0 * LD + c * 4;
+      float* ls = ks + (kKT + ROWS) * LD + r0;
+      loader.template load<false>(p, w.h, ks, nullptr, LD);
+      const int tok0 = t * p.tile_tokens, rows = min(p.tile_tokens, w.v.n - tok0) * p.G;
+      const float* q = static_cast<const float*>(p.q) + (w.v.r0 + tok0) * p.q_stride + w.h * p.G * D + c * 4;
+      const float* lse = p.lse + static_cast<long long>(w.v.r0 + tok0) * p.Hq + w.h * p.G;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key0 + ty * 4 + i < limit) sum[i] += exp2f(fmaf(s[i][j], p.scale_log2, -lse2));
+      for (int i = 0; i < kRows; ++i) {
+        const bool in = r0 + i * kStep < rows;
+        cp_async16_or_zero(qs + i * kStep * LD, in ? q + tok[i] * p.q_stride + head[i] * D : q, in);
+        if (c == 0 && in)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ls + i * kStep)),
+                       "l"(lse + tok[i] * p.Hq + head[i])
+                       : "memory");
+      }
+      more = ++w.u < w.u1;
+      if (threadIdx.x == 0) steps_s[put % kStages] = {w.b, w.h, kb, t, t + 1 == tiles || !more, first, w.v};
+      ++put;
+      if (++t == tiles) {
+        t = 0;
+        first = true;
+        if (++kb == blocks) {
+          kb = 0;
+          while (more) {                       // the next head that has any
+            if (++w.h == p.Hkv) {
+              w.h = 0;
+              w.v = w.next;
+              walk_to(p, w, w.b + 1);
+              head_size();
+            }
+            if (blocks > 0 && tiles > 0) break;
+          }
         }
       }
+      if (more) loader.look(p, {w.b, kb * kKT, w.v.len});
     }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int at = 0; at < put; ++at) {
+    cp_async_wait<kStages - 2>();
+    __syncthreads();                           // step `at` is there, and the step before is read
+    issue();
+    const WeightStep& d = steps_s[at % kStages];
+    const float* ks = sm + at % kStages * C::kFloats;
+    const float* qs = ks + kKT * LD;
+    const float* ls = qs + ROWS * LD;
+    const int key0 = d.kb * kKT + ty * 4, tok0 = d.t * p.tile_tokens;
+    const int rows = min(p.tile_tokens, d.v.n - tok0) * p.G;
+    // the scores that the sums go to, asked for now
+    float* scores = p.scores + (static_cast<long long>(d.b) * p.Hkv + d.h) * paged_cap(p) + key0;
+    const bool adds = tx == 0 && d.last && d.first;
+    float old[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) old[i] = adds && key0 + i < d.v.len ? scores[i] : 0.f;
+    float s[4][RPT];
+    dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
 #pragma unroll
-      for (int d = 8; d; d >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
-    if (tx == 0) {
+    for (int j = 0; j < RPT; ++j) {
+      const int r = tx + 16 * j;
+      if (r < rows) {
+        const int limit = key_limit(p, d.b, d.v, tok0 + r / p.G);
+        const float lse2 = ls[r] * 1.4426950408889634f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + ty * 4 + i;
-        if (g.t0 > 0)
-          p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + ty * 4 + i] = sum[i];
-        else if (key < g.v.len)
-          p.scores[(static_cast<long long>(g.b) * p.Hkv + g.h) * paged_cap(p) + key] += sum[i];
+        for (int i = 0; i < 4; ++i)
+          if (key0 + i < limit) sum[i] += exp2f(fmaf(s[i][j], p.scale_log2, -lse2));
       }
     }
-    if (g.t0 > 0 && threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(g.b, g.h, g.kb, 1);
+    if (!d.last) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int k = 8; k; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
+      if (adds) {
+        if (key0 + i < d.v.len) scores[i] = old[i] + sum[i];
+      } else if (tx == 0) {
+        p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + ty * 4 + i] = sum[i];
+      }
+      sum[i] = 0.f;
+    }
+    if (!d.first && threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(d.b, d.h, d.kb, 1);
   }
 }
 
@@ -330,7 +407,7 @@ cudaError_t attend(cudaStream_t s, const PagedParams& p) {
 }
 template <int D, int ROWS>
 cudaError_t weights(cudaStream_t s, const PagedParams& p) {
-  constexpr size_t smem = sizeof(float) * (ROWS + kKT) * (D + 4);
+  constexpr size_t smem = WeightsCfg<D, ROWS>::kSmem;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_weights_simt_kernel<D, ROWS>),
