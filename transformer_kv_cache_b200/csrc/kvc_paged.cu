@@ -132,13 +132,12 @@ void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
     return;
   }
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
-  const int tile = per_seq <= 16 ? 16 : 64;
-  p->tile_tokens = p->item_tokens = tile / p->G;
+  p->tile_tokens = p->item_tokens = (per_seq <= 16 ? 16 : 64) / p->G;
   p->key_tile = 64;
   p->key_shift = 6;
   p->streams = 1;
   p->slot_rows = p->key_tile;
-  if (p->D == 64 || tile == 16) p->grid *= 2;  // CTAs that fit an SM
+  p->grid *= 2;                                // CTAs that fit an SM
 }
 
 Layout attend_layout(const PagedParams& p) {

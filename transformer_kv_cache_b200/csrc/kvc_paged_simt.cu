@@ -248,8 +248,10 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
 template <int D, int ROWS>
 struct WeightsCfg {
   static constexpr int kLD = D + 4;
-  // as many as leave room for two CTAs of an SM, or one where a step takes 67 KB
-  static constexpr int kStages = D == 64 ? (ROWS == 16 ? 4 : 3) : (ROWS == 16 ? 2 : 3);
+  // as many as leave room for two CTAs of an SM. Where a step takes 68 KB the CTAs of an SM cover one
+  // another's loads instead (2 x 300 rows over 4,000 tokens, 128 dims: 142 us, and with three stages of
+  // one CTA 173)
+  static constexpr int kStages = D == 64 ? (ROWS == 16 ? 3 : 2) : (ROWS == 16 ? 2 : 1);
   static constexpr int kFloats = (kKT + ROWS) * kLD + ROWS;
   static constexpr size_t kSmem = sizeof(float) * kStages * kFloats;
 };
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   extern __shared__ __align__(16) float sm[];  // [stage][keys | rows][LD], [rows] log-sum-exp
   __shared__ long long plan_s[kPlanWords + kThreads / 32];
   __shared__ WeightStep steps_s[kStages];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;            // of ROWS = 64
   Walk w = plan_walk(p, plan_s, [&](int, const SeqView& v) { return weight_head_units(p, v); });
   if (threadIdx.x == 0) p.part_id[blockIdx.x] = make_int4(0, 0, 0, 0);
   // the step that is looked up; its head's key blocks and query tiles
@@ -339,46 +341,92 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   };
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) issue();
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  // The keys whose sums this thread holds, kKeys from `mine` on; `writes`: the whole of them in the end.
+  const int lane = threadIdx.x & 31, part = lane & 15;
+  constexpr int kKeys = ROWS == 16 ? 1 : 4;
+  const int mine = ROWS == 16 ? (static_cast<int>(threadIdx.x) >> 5) * 8 + (lane >> 4) * 4 + (part >> 2) : ty * 4;
+  const bool writes = ROWS == 16 ? (part & 3) == 0 : tx == 0;
+  float sum[kKeys] = {};
 #pragma unroll 1
-  for (int at = 0; at < put; ++at) {
-    cp_async_wait<kStages - 2>();
+  for (int at = 0;; ++at) {
+    if (kStages == 1) {
+      __syncthreads();                         // the step before is read
+      issue();
+    }
+    if (at == put) break;
+    cp_async_wait<kStages == 1 ? 0 : kStages - 2>();
     __syncthreads();                           // step `at` is there, and the step before is read
-    issue();
+    if (kStages > 1) issue();
     const WeightStep& d = steps_s[at % kStages];
     const float* ks = sm + at % kStages * C::kFloats;
     const float* qs = ks + kKT * LD;
     const float* ls = qs + ROWS * LD;
-    const int key0 = d.kb * kKT + ty * 4, tok0 = d.t * p.tile_tokens;
+    const int key0 = d.kb * kKT + mine, tok0 = d.t * p.tile_tokens;
     const int rows = min(p.tile_tokens, d.v.n - tok0) * p.G;
     // the scores that the sums go to, asked for now
     float* scores = p.scores + (static_cast<long long>(d.b) * p.Hkv + d.h) * paged_cap(p) + key0;
-    const bool adds = tx == 0 && d.last && d.first;
-    float old[4];
+    const bool adds = writes && d.last && d.first;
+    float old[kKeys];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) old[i] = adds && key0 + i < d.v.len ? scores[i] : 0.f;
-    float s[4][RPT];
-    dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
+    for (int i = 0; i < kKeys; ++i) old[i] = adds && key0 + i < d.v.len ? scores[i] : 0.f;
+    auto gain = [&](float s, int key, int r) {
+      const float e = exp2f(fmaf(s, p.scale_log2, -1.4426950408889634f * ls[r]));
+      return key < key_limit(p, d.b, d.v, tok0 + r / p.G) ? e : 0.f;
+    };
+    if constexpr (ROWS == 16) {
+      // a lane has 4 keys by 4 rows of a sixteenth of the dims
+      const float* k4 = ks + (mine & ~3) * LD + part * 4;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 4) {
+        const float* q4 = qs + r0 * LD + part * 4;
+        float a[16];
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-      const int r = tx + 16 * j;
-      if (r < rows) {
-        const int limit = key_limit(p, d.b, d.v, tok0 + r / p.G);
-        const float lse2 = ls[r] * 1.4426950408889634f;
+        for (int i = 0; i < 16; ++i) a[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key0 + i < limit) sum[i] += exp2f(fmaf(s[i][j], p.scale_log2, -lse2));
+        for (int x = 0; x < D; x += 64) {
+          float4 k[4], q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            k[i] = load4(k4 + i * LD + x);
+            q[i] = load4(q4 + i * LD + x);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 u = k[i >> 2], v = q[i & 3];
+            a[i] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, a[i]))));
+          }
+        }
+        // summed over the 16 lanes, product `part` in lane `part`
+#pragma unroll
+        for (int n = 8; n; n >>= 1) {
+          const bool upper = part & n;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? a[i] : a[i + n], n);
+            a[i] = (upper ? a[i + n] : a[i]) + other;
+          }
+        }
+        const int r = r0 + (part & 3);
+        if (r < rows) sum[0] += gain(a[0], key0, r);
       }
+    } else {
+      float s[4][RPT];
+      dots<D, 4, RPT>(ks + ty * 4 * LD, LD, 1, qs + tx * LD, LD, 16, s);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j)
+        if (tx + 16 * j < rows)
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) sum[i] += gain(s[i][j], key0 + i, tx + 16 * j);
     }
     if (!d.last) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kKeys; ++i) {
 #pragma unroll
-      for (int k = 8; k; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
+      for (int k = ROWS == 16 ? 2 : 8; k; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
       if (adds) {
         if (key0 + i < d.v.len) scores[i] = old[i] + sum[i];
-      } else if (tx == 0) {
-        p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + ty * 4 + i] = sum[i];
+      } else if (writes) {
+        p.part_w[static_cast<long long>(blockIdx.x) * p.slot_rows + mine + i] = sum[i];
       }
       sum[i] = 0.f;
     }
