@@ -58,6 +58,40 @@ __device__ __forceinline__ void dots(const float* a, int lda, int sa, const floa
   }
 }
 
+// Scores of 4 keys by 4 rows in 16 lanes, a sixteenth of the dims in each (64 products for eight loads,
+// which bound these kernels); summed over the lanes, that of key `part / 4` and row `part % 4` ends
+// in lane `part`. k4 and q4 are the lane's first 16 bytes of the first key and row.
+template <int D, int LD>
+__device__ __forceinline__ float dots_by_lanes(const float* k4, const float* q4, int part) {
+  float a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = 0.f;
+#pragma unroll
+  for (int x = 0; x < D; x += 64) {
+    float4 k[4], q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k[i] = load4(k4 + i * LD + x);
+      q[i] = load4(q4 + i * LD + x);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float4 u = k[i >> 2], v = q[i & 3];
+      a[i] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, a[i]))));
+    }
+  }
+#pragma unroll
+  for (int n = 8; n; n >>= 1) {
+    const bool upper = part & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? a[i] : a[i + n], n);
+      a[i] = (upper ? a[i + n] : a[i]) + other;
+    }
+  }
+  return a[0];
+}
+
 // 16 bytes to shared memory behind the registers' back, or zeros where `there` is false.
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
@@ -104,13 +138,13 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One segment in tiles of ROWS query rows; sm holds [rows][LD] queries, two stages of [kKT][LD] keys
+// One segment in tiles of 64 query rows; sm holds [rows][LD] queries, two stages of [kKT][LD] keys
 // and values, [rows][LP] weights.
-template <int D, int ROWS, int MAXROWS>
+template <int D>
 __device__ __forceinline__ void attend_segment(const PagedParams& p, const Segment& g, float* sm) {
-  constexpr int LD = D + 4, RPT = ROWS / 16, LP = kKT + 4;
+  constexpr int LD = D + 4, ROWS = 64, RPT = ROWS / 16, LP = kKT + 4;
   float* qs = sm;
-  float* kv = qs + MAXROWS * LD;               // [stage][K, V][kKT][LD]
+  float* kv = qs + ROWS * LD;                  // [stage][K, V][kKT][LD]
   float* ps = kv + 4 * kKT * LD;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int t0 = g.i * item_tokens(p, g.b);
@@ -226,6 +260,145 @@ __device__ __forceinline__ void attend_segment(const PagedParams& p, const Segme
   }
 }
 
+// One segment in tiles of 16 query rows, in three phases of a key tile: scores (a warp has 8 keys),
+// softmax (a warp has two rows), sums (16 bytes of the dims, 4 rows and some of the keys to a thread:
+// all threads have keys however few the rows are, and are joined at the end of the segment).
+// MAXROWS: query rows that the kernel's shared memory is laid out for.
+template <int D, int MAXROWS>
+__device__ __forceinline__ void attend_few(const PagedParams& p, const Segment& g, float* sm) {
+  constexpr int LD = D + 4, LP = kKT + 4, kChunks = D / 4, kGroups = kThreads / kChunks;
+  float* qs = sm;
+  float* kv = qs + MAXROWS * LD;               // [stage][K, V][kKT][LD]
+  float* ss = kv + 4 * kKT * LD;               // [row][LP] scores
+  float* pt = ss + 16 * LP;                    // [key][16 rows] weights
+  float* fs = pt + kKT * 16;                   // [row] factors of what was summed before; at the end 1 / sum
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 15;
+  const int t0 = g.i * item_tokens(p, g.b);
+  const int tokens = min(item_tokens(p, g.b), g.v.n - t0), rows = tokens * p.G;
+  const int quads = rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
+  const int c = threadIdx.x % kChunks, quad = threadIdx.x / kChunks % quads, k_first = threadIdx.x / kChunks / quads,
+            k_step = kGroups / quads;
+  KeyLoader<D> loader;
+  loader.look(p, key_tile_at(p, g, g.k0));
+  __syncthreads();                             // the segment before is read
+  loader.template load<true>(p, g.h, kv, kv + kKT * LD, LD);
+  cp_async_commit();
+  load_queries<D, LD, 16>(p, g.v, g.h, t0, rows, qs);
+  float m[2], l[2];                            // of rows 2 warp, + 1
+  int limit[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int at = 2 * warp + r;
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.f;
+    limit[r] = at < rows ? key_limit(p, g.b, g.v, t0 + at / p.G) : 0;
+  }
+  float acc[4][4] = {};                        // [row][dim]
+  if (g.k0 + 1 < g.k1) loader.look(p, key_tile_at(p, g, g.k0 + 1));
+#pragma unroll 1
+  for (int kt = g.k0; kt < g.k1; ++kt) {
+    const int st = (kt - g.k0) & 1;
+    const float* ks = kv + st * 2 * kKT * LD;
+    const float* vs = ks + kKT * LD;
+    if (kt + 1 < g.k1) {
+      float* next = kv + (st ^ 1) * 2 * kKT * LD;
+      loader.template load<true>(p, g.h, next, next + kKT * LD, LD);
+      cp_async_commit();
+      if (kt + 2 < g.k1) loader.look(p, key_tile_at(p, g, kt + 2));
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    const int key4 = warp * 8 + (lane >> 4) * 4;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 4)
+      ss[(r0 + (part & 3)) * LP + key4 + (part >> 2)] =
+          dots_by_lanes<D, LD>(ks + key4 * LD + part * 4, qs + r0 * LD + part * 4, part);
+    __syncthreads();
+    const KeyTile tile = key_tile_at(p, g, kt);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int at = 2 * warp + r;
+      if (at >= rows) break;
+      const int end = (tile.b == g.b ? limit[r] : tile.len) - tile.key0;
+      const float s0 = lane < end ? ss[at * LP + lane] * p.scale_log2 : -CUDART_INF_F;
+      const float s1 = lane + 32 < end ? ss[at * LP + lane + 32] * p.scale_log2 : -CUDART_INF_F;
+      float mx = fmaxf(s0, s1);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float m_new = fmaxf(m[r], mx);
+      const float base = m_new == -CUDART_INF_F ? 0.f : m_new;       // nothing visible yet: every weight is 0
+      const float f = exp2f(m[r] - base), e0 = exp2f(s0 - base), e1 = exp2f(s1 - base);
+      pt[lane * 16 + at] = e0;
+      pt[(lane + 32) * 16 + at] = e1;
+      float sum = e0 + e1;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[r] = l[r] * f + sum;
+      m[r] = m_new;
+      if (lane == 0) fs[at] = f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = fs[4 * quad + r];        // of rows that there are not: nothing that is kept
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][i] *= f;
+    }
+#pragma unroll 4
+    for (int k = k_first; k < kKT; k += k_step) {
+      const float4 v = load4(vs + k * LD + c * 4), e = load4(pt + k * 16 + 4 * quad);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = r == 0 ? e.x : r == 1 ? e.y : r == 2 ? e.z : e.w;
+        acc[r][0] = fmaf(x, v.x, acc[r][0]);
+        acc[r][1] = fmaf(x, v.y, acc[r][1]);
+        acc[r][2] = fmaf(x, v.z, acc[r][2]);
+        acc[r][3] = fmaf(x, v.w, acc[r][3]);
+      }
+    }
+    __syncthreads();                           // the stage, the weights and the factors are read
+  }
+  // the groups' sums to shared memory ([group of keys][row][D], in the first K), then joined in order
+  const bool whole = g.k0 == 0 && g.k1 == g.nk && writes_rows(p, g.v, g.i);
+  auto place = [&](int at, long long& out, long long& slot) {
+    const int row = g.v.r0 + t0 + at / p.G, hq = g.h * p.G + at % p.G;
+    out = static_cast<long long>(row) * p.Hq + hq;
+    slot = g.k0 == 0 ? row_slot(p, g.b, 0, row, hq) : cta_slot(p, blockIdx.x, at);
+  };
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    *reinterpret_cast<float4*>(kv + ((k_first * quads + quad) * 4 + r) * D + c * 4) =
+        make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int at = 2 * warp + r;
+    if (at >= rows || lane > 0) break;
+    long long out, slot;
+    place(at, out, slot);
+    fs[at] = whole ? (l[r] == 0.f ? 0.f : 1.f / l[r]) : 1.f;
+    if (!whole) p.part_ml[slot] = make_float2(m[r], l[r]);
+    else if (p.lse) p.lse[out] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  const int at = threadIdx.x / kChunks;        // a thread for 16 bytes of a row, kGroups rows at once
+#pragma unroll 1
+  for (int r = at; r < rows; r += kGroups) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < k_step; ++k) {
+      const float4 x = load4(kv + (k * quads * 4 + r) * D + c * 4);
+      sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+    }
+    const float f = fs[r];
+    long long out, slot;
+    place(r, out, slot);
+    float* dst = whole ? static_cast<float*>(p.o) + out * D : p.part_o + slot * D;
+    *reinterpret_cast<float4*>(dst + c * 4) = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+  }
+}
+
 // OWN and PREFIX: query rows of a tile of a sequence's own keys and of the prefix's.
 template <int D, int OWN, int PREFIX>
 __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const PagedParams p) {
@@ -238,8 +411,9 @@ __global__ void __launch_bounds__(kThreads) paged_attend_simt_kernel(const Paged
   walk_to_item(p, w);
   Segment g;
   while (next_segment(p, w, g)) {
-    if (OWN != PREFIX && g.b < 0) attend_segment<D, PREFIX, kMax>(p, g, sm);
-    else attend_segment<D, OWN, kMax>(p, g, sm);
+    const bool few = OWN == PREFIX || g.b >= 0 ? OWN == 16 : PREFIX == 16;
+    if (few) attend_few<D, kMax>(p, g, sm);
+    else attend_segment<D>(p, g, sm);
   }
 }
 
@@ -374,40 +548,12 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
       return key < key_limit(p, d.b, d.v, tok0 + r / p.G) ? e : 0.f;
     };
     if constexpr (ROWS == 16) {
-      // a lane has 4 keys by 4 rows of a sixteenth of the dims
       const float* k4 = ks + (mine & ~3) * LD + part * 4;
 #pragma unroll 1
       for (int r0 = 0; r0 < rows; r0 += 4) {
-        const float* q4 = qs + r0 * LD + part * 4;
-        float a[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = 0.f;
-#pragma unroll
-        for (int x = 0; x < D; x += 64) {
-          float4 k[4], q[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            k[i] = load4(k4 + i * LD + x);
-            q[i] = load4(q4 + i * LD + x);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 u = k[i >> 2], v = q[i & 3];
-            a[i] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, a[i]))));
-          }
-        }
-        // summed over the 16 lanes, product `part` in lane `part`
-#pragma unroll
-        for (int n = 8; n; n >>= 1) {
-          const bool upper = part & n;
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            const float other = __shfl_xor_sync(0xffffffffu, upper ? a[i] : a[i + n], n);
-            a[i] = (upper ? a[i + n] : a[i]) + other;
-          }
-        }
+        const float x = dots_by_lanes<D, LD>(k4, qs + r0 * LD + part * 4, part);
         const int r = r0 + (part & 3);
-        if (r < rows) sum[0] += gain(a[0], key0, r);
+        if (r < rows) sum[0] += gain(x, key0, r);
       }
     } else {
       float s[4][RPT];
@@ -437,7 +583,9 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
 template <int D, int OWN, int PREFIX>
 cudaError_t attend(cudaStream_t s, const PagedParams& p) {
   constexpr int kMax = OWN > PREFIX ? OWN : PREFIX;
-  constexpr size_t smem = sizeof(float) * (kMax * (D + 4) + 4 * kKT * (D + 4) + kMax * (kKT + 4));
+  // scores, weights and factors of the few-row form, or weights
+  constexpr int kLast = kMax == 16 ? 16 * (kKT + 4) + kKT * 16 + 16 : kMax * (kKT + 4);
+  constexpr size_t smem = sizeof(float) * (kMax * (D + 4) + 4 * kKT * (D + 4) + kLast);
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_attend_simt_kernel<D, OWN, PREFIX>),
