@@ -304,54 +304,59 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   const int b = find_sequence(p.row_start, p.B, row);
   const int h = hq / p.G, g = hq % p.G;
   const int parts = parts_of(p);
-  // per part: units of the item, its first unit (without the sequence's), and the row's place
-  int nk0 = 0, nk1 = 0, at0 = 0, at1 = 0, tile0 = 0, tile1 = 0;
-  long long first0 = 0, first1 = 0;
-  bool split0 = false, split1 = false, whole = false;
-  auto look = [&](int s, int& nk, int& at, int& tile, long long& first, bool& split) {
+  // Half of the lanes look up the row's part of the prefix, the others its own (one place in the code
+  // for both): the item's units up to its last key tile's first, its first unit (without the
+  // sequence's), and the row's place.
+  const bool second = lane >= LANES / 2;
+  int nk = 0, place = 0;                               // row of the tile << 2 | tile << 1 | the keys are split
+  long long first = 0;
+  bool whole = false, mine = hq < p.Hq;
+  if (b >= 0 && (second || parts == 2)) {
+    const int s = second ? b : -1;
     const SeqView v = seq_view(p, s);
     const int t = row - v.r0;
-    if (t < 0 || t >= v.n) return;
-    const int it = item_tokens(p, s), item = t / it, in = t - item * it;
-    // the item's units but for those of its last key tile behind the first one, which counts
-    nk = item_tiles(p, s, v, item) > 0 ? (item_tiles(p, s, v, item) - 1) * tile_cost(p, v, item) + 1 : 0;
-    first = h * head_units(p, s, v) + units_before(p, s, v, item);
-    split = p.streams == 2 && !two_tiles(p, v, item);
-    tile = p.streams == 2 ? in / p.tile_tokens : 0;
-    at = (in - tile * p.tile_tokens) * p.G + g;
-    whole = writes_rows(p, v, item);
-  };
-  if (b >= 0) {
-    if (parts == 2) look(-1, nk0, at0, tile0, first0, split0);
-    look(b, nk1, at1, tile1, first1, split1);
+    if (t >= 0 && t < v.n) {
+      const int it = item_tokens(p, s), item = t / it, in = t - item * it;
+      const int tiles = item_tiles(p, s, v, item);
+      if (tiles > 0) nk = (tiles - 1) * tile_cost(p, v, item) + 1;
+      // the heads before, then the items before
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k)
+        first += (k == 0 ? h : 1) * units_before(p, s, v, k == 0 ? seq_items(p, s, v) : item);
+      const int tile = p.streams == 2 ? in / p.tile_tokens : 0;
+      place = ((in - tile * p.tile_tokens) * p.G + g) << 2 | tile << 1 | (p.streams == 2 && !two_tiles(p, v, item));
+      whole = second && writes_rows(p, v, item);
+    }
   }
   griddep_wait();
   griddep_launch_dependents();
   if (b < 0) return;                                   // behind the last sequence: left as it was
   const long long U = __ldcg(p.plan), own = __ldcg(p.plan + 1 + b);
   // the partials in the order of their keys: per part its CTAs' pieces, per piece its streams
-  int c0 = 0, c1 = 0, n0 = 0, n1 = 0;
-  bool mine = hq < p.Hq;
-  if (nk0 > 0) {
-    c0 = static_cast<int>(quotient(first0, U));
-    n0 = (static_cast<int>(quotient(first0 + nk0 - 1, U)) - c0 + 1) * (split0 ? 2 : 1);
+  int c = 0, n = 0;
+  if (nk > 0) {
+    const long long u0 = first + (second ? own : 0);
+    int end = 0;                                       // its CTA, then that of the first unit
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      end = c;
+      c = static_cast<int>(quotient(k == 0 ? u0 + nk - 1 : u0, U));
+    }
+    const int pieces = end - c + 1;
+    n = pieces == 1 && whole ? -1 : pieces << (place & 1);
   }
-  if (nk1 > 0) {
-    const long long u0 = own + first1;
-    c1 = static_cast<int>(quotient(u0, U));
-    const int pieces = static_cast<int>(quotient(u0 + nk1 - 1, U)) - c1 + 1;
-    if (pieces == 1 && whole) mine = false;            // written by its CTA
-    n1 = pieces * (split1 ? 2 : 1);
-  }
+  const int c0 = __shfl_sync(0xffffffffu, c, 0, LANES), c1 = __shfl_sync(0xffffffffu, c, LANES / 2, LANES);
+  const int n0 = __shfl_sync(0xffffffffu, n, 0, LANES), n1 = __shfl_sync(0xffffffffu, n, LANES / 2, LANES);
+  const int place0 = __shfl_sync(0xffffffffu, place, 0, LANES),
+            place1 = __shfl_sync(0xffffffffu, place, LANES / 2, LANES);
+  if (n1 < 0) mine = false;                            // written by its CTA
   const int total = mine ? n0 + n1 : 0;
   auto slot_of = [&](int i) {
     const bool k = i >= n0;
-    const bool split = k ? split1 : split0;
-    const int j = k ? i - n0 : i;
-    const int piece = split ? j >> 1 : j, stream = split ? j & 1 : 0;
+    const int at = k ? place1 : place0, j = k ? i - n0 : i;
+    const int piece = at & 1 ? j >> 1 : j, stream = at & 1 ? j & 1 : 0;
     if (piece == 0) return row_slot(p, k ? b : -1, stream, row, hq);
-    return cta_slot(p, (k ? c1 : c0) + piece,
-                    (split ? stream : k ? tile1 : tile0) * (p.slot_rows / p.streams) + (k ? at1 : at0));
+    return cta_slot(p, (k ? c1 : c0) + piece, (at & 1 ? stream : at >> 1 & 1) * (p.slot_rows / p.streams) + (at >> 2));
   };
   float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
