@@ -520,7 +520,9 @@ KVC_API kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void* k_
  * that sees nothing gets O = 0 and an LSE of -inf. The prefix's keys and values are read for
  * the whole batch at once. o_dev is densely packed. bf16 runs on tcgen05 tensor cores (fp32
  * logits, statistics and accumulation, weights rounded to bf16 for the second product), fp32
- * in fp32 arithmetic. Logits are to stay below 2^20 in magnitude, as for kvc_attend.
+ * in fp32 arithmetic. Logits are to stay below 2^20 in magnitude, as for kvc_attend. A key
+ * that is no number makes the rows that see it NaN; a value that is none can reach every row
+ * of its sequence in the call (hidden keys have a weight of 0, and 0 x NaN is NaN).
  * Errors: KVC_ERR_ARG (batch, pointers, strides, more than 2^32 row-heads, a workspace
  * that is too small), KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
@@ -531,9 +533,9 @@ KVC_API kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void* q_
  * scores[b][h][j] += sum over the sequence's rows i and the query heads of KV head h of
  * e^(softmax_scale q_i . k_j - lse_i), over the rows that see slot j (`causal` as in
  * kvc_paged_attend, whose q_dev and lse_dev these are; another LSE, e.g. over a window of
- * keys, is as good). The sums are fp32, in an order that depends on the sizes alone. A
- * row with an LSE of +inf adds nothing. Errors: as kvc_paged_attend; KVC_ERR_ARG without
- * scores. */
+ * keys, is as good, where the products q_i . k_j that the row sees are finite or its LSE is
+ * not). The sums are fp32, in an order that depends on the sizes alone. A row with an LSE of
+ * +inf adds nothing. Errors: as kvc_paged_attend; KVC_ERR_ARG without scores. */
 KVC_API kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
                                      const float* lse_dev, int32_t rows, const int32_t* row_start_dev,
                                      int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream);

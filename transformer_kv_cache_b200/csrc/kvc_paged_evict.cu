@@ -23,6 +23,10 @@
 // Moves. Bound by memory (two rows read and written each). The selection looks the pages up, so
 // that a move is two dependent loads, its entry in the list and its rows, and a thread has kUnroll
 // moves under way.
+//
+// 64 sequences of 8 heads of 4,097 tokens, one of which goes: 14 us a step with the append, most of it
+// the three launches' own. 4 sequences of up to 32,768 tokens cut to 4,096: 49 us (120 MB: 2.4 TB/s),
+// a third of it the selection, three passes whose barriers a cluster of four waits for.
 #include <algorithm>
 
 #include "kvc_paged.cuh"

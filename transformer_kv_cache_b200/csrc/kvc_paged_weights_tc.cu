@@ -25,7 +25,10 @@
 // keys' bytes are the bound: 4 sum warps a stream. Else the exponentials are: 8 sum warps a stream,
 // four for a query tile's first 64 rows and four for the others (the halves of a key's sum meet in
 // shared memory at the end of a block), so that four warps a scheduler cover one another's waits,
-// and as much room for query tiles as for key tiles.
+// and as much room for query tiles as for key tiles. The frame of 1,004 rows below takes 134 us with
+// four sum warps a stream and one issuer. 32 sequences of 4,096 to 8,192 tokens, a row of 32 heads
+// over 8 KV heads of 128 dims each: 70 us, 5.9 TB/s. A frame of 1,004 rows of 16 heads of 64 dims over
+// 16,064 keys: 99 us, 2.6 x 10^12 exponentials a second, where the MUFU alone gives 4.5 x 10^12.
 #include "kvc_paged.cuh"
 #include "kvc_paged_math.cuh"
 
