@@ -131,8 +131,10 @@ void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
     p->streams = 1;
     return;
   }
+  // tiles of 32 rows, of which only fours that there are cost anything, where a sequence has no more
+  // (16 sequences of 4 rows of 6 heads: 82 us, in tiles of 64 120; of 4 heads' one row: 76, in 16 72)
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
-  p->tile_tokens = p->item_tokens = (per_seq <= 16 ? 16 : 64) / p->G;
+  p->tile_tokens = p->item_tokens = (per_seq <= 32 ? 32 : 64) / p->G;
   p->key_tile = 64;
   p->key_shift = 6;
   p->streams = 1;

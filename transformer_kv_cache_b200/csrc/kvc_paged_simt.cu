@@ -4,7 +4,7 @@
 // Attention: one pass over an item's keys with the running maximum and sum of the softmax, the
 // next tile's keys and values arriving by cp.async under this one's products. A tile is 16 rows
 // where sequences have no more, else 64, the prefix's chosen by the batch's rows. Weights: a block
-// of keys with a tile of 16 or 64 rows, a key's sum over the rows in one thread or half-warp.
+// of keys with a tile of 32 or 64 rows, a key's sum over the rows in one thread or half-warp.
 //
 // What shared memory gives back (512 bytes in four cycles for a load of 16 bytes a lane) bounds the
 // products: 64 rows are 4 x 4 of them to a thread, 16 x 16 threads, eight loads for 64 FFMA, twice the
@@ -430,7 +430,7 @@ struct WeightsCfg {
   // as many as leave room for two CTAs of an SM. Where a step takes 68 KB the CTAs of an SM cover one
   // another's loads instead (2 x 300 rows over 4,000 tokens, 128 dims: 142 us, and with three stages of
   // one CTA 173)
-  static constexpr int kStages = D == 64 ? (ROWS == 16 ? 3 : 2) : (ROWS == 16 ? 2 : 1);
+  static constexpr int kStages = D == 64 ? (ROWS == 32 ? 3 : 2) : (ROWS == 32 ? 2 : 1);
   static constexpr int kFloats = (kKT + ROWS) * kLD + ROWS;
   static constexpr size_t kSmem = sizeof(float) * kStages * kFloats;
 };
@@ -522,9 +522,9 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
   for (int i = 0; i < kStages - 1; ++i) issue();
   // The keys whose sums this thread holds, kKeys from `mine` on; `writes`: the whole of them in the end.
   const int lane = threadIdx.x & 31, part = lane & 15;
-  constexpr int kKeys = ROWS == 16 ? 1 : 4;
-  const int mine = ROWS == 16 ? (static_cast<int>(threadIdx.x) >> 5) * 8 + (lane >> 4) * 4 + (part >> 2) : ty * 4;
-  const bool writes = ROWS == 16 ? (part & 3) == 0 : tx == 0;
+  constexpr int kKeys = ROWS == 32 ? 1 : 4;
+  const int mine = ROWS == 32 ? (static_cast<int>(threadIdx.x) >> 5) * 8 + (lane >> 4) * 4 + (part >> 2) : ty * 4;
+  const bool writes = ROWS == 32 ? (part & 3) == 0 : tx == 0;
   float sum[kKeys] = {};
 #pragma unroll 1
   for (int at = 0;; ++at) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
       const float e = exp2f(fmaf(s, p.scale_log2, -1.4426950408889634f * ls[r]));
       return key < key_limit(p, d.b, d.v, tok0 + r / p.G) ? e : 0.f;
     };
-    if constexpr (ROWS == 16) {
+    if constexpr (ROWS == 32) {
       const float* k4 = ks + (mine & ~3) * LD + part * 4;
 #pragma unroll 1
       for (int r0 = 0; r0 < rows; r0 += 4) {
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_simt_kernel(const Page
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
 #pragma unroll
-      for (int k = ROWS == 16 ? 2 : 8; k; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
+      for (int k = ROWS == 32 ? 2 : 8; k; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
       if (adds) {
         if (key0 + i < d.v.len) scores[i] = old[i] + sum[i];
       } else if (writes) {
@@ -625,9 +625,9 @@ cudaError_t launch_paged_attend_simt(cudaStream_t s, const PagedParams& p) {
 }
 
 cudaError_t launch_paged_weights_simt(cudaStream_t s, const PagedParams& p) {
-  const bool few = p.tile_tokens * p.G <= 16;
-  if (p.D == 64) return few ? weights<64, 16>(s, p) : weights<64, 64>(s, p);
-  return few ? weights<128, 16>(s, p) : weights<128, 64>(s, p);
+  const bool few = p.tile_tokens * p.G <= 32;
+  if (p.D == 64) return few ? weights<64, 32>(s, p) : weights<64, 64>(s, p);
+  return few ? weights<128, 32>(s, p) : weights<128, 64>(s, p);
 }
 
 }  // namespace kvc
