@@ -108,6 +108,41 @@ def test_weights(kvc, shape, dtype):
     assert torch.equal(c.scores.cpu()[past], t.scores[past])  # slots past the length: untouched
 
 
+# sequences around a warp's 32 and a block's 384 and 640 threads (who makes the schedule), every one of which
+# ends inside a page of any size, with segments of one key tile and more, and rows that fill one tile or two
+SCHEDULES = {
+    "31 and a prefix": dict(rows=[1] * 31, lengths=[1 + 9 * i for i in range(31)], hq=8, hkv=2, d=128, page=256,
+                            prefix=201),
+    "32 and a prefix": dict(rows=[1 + i % 4 for i in range(32)], lengths=[5 + 11 * i for i in range(32)], hq=4, hkv=2,
+                            d=64, page=128, prefix=77),
+    "32": dict(rows=[2] * 32, lengths=[3 + 13 * i for i in range(32)], hq=6, hkv=2, d=128, page=64),
+    "33": dict(rows=[1 + i % 3 for i in range(33)], lengths=[3 + 13 * i for i in range(33)], hq=6, hkv=2, d=64, page=32),
+    "385": dict(rows=[1] * 385, lengths=[1 + (7 * i) % 150 for i in range(385)], hq=2, hkv=1, d=128, page=128, prefix=130),
+    "650 of many rows": dict(rows=[1 + i % 2 for i in range(649)] + [90], lengths=[2 + i % 19 for i in range(649)] + [777],
+                             hq=2, hkv=1, d=64, page=256, prefix=9),
+    "17 to 32 rows of a head": dict(rows=[5, 6, 8, 7, 8], lengths=[300, 65, 8, 129, 1000], hq=12, hkv=3, d=128, page=32),
+    "one row tile and two": dict(rows=[100, 130, 256, 257, 1], lengths=[500, 131, 256, 700, 90], hq=2, hkv=2, d=64,
+                                 page=128, prefix=120),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SCHEDULES)
+def test_schedules(kvc, shape, dtype):
+    """Attention and weights over batches whose schedules differ, both ways of masking."""
+    for causal in (True, False):
+        t, _ = build(SCHEDULES[shape], dtype, seed=31)
+        o, lse = run_attend(kvc, t, causal)
+        check_attend(t, causal, o, lse)
+        c = copy.deepcopy(t).to(DEV)
+        batch = c.handle(kvc)
+        kvc.kvc_paged_weights(batch, c.q, lse.to(DEV), c.row_start, c.workspace(kvc, batch), causal=causal)
+        torch.cuda.synchronize()
+        assert int(c.error) == 0
+        ref, bound = weights64(t, lse, causal)
+        assert ((c.scores.cpu().double() - ref).abs() <= bound).all()
+
+
 def test_weights_sum_to_the_rows(kvc):
     """Without a prefix every row's weights sum to 1: the scores gain rows x group in all."""
     t, causal = build("chunks, causal", "bf16", seed=3)
