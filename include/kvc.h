@@ -533,9 +533,10 @@ KVC_API kvc_status kvc_paged_attend(const kvc_paged_batch* batch, const void* q_
  * scores[b][h][j] += sum over the sequence's rows i and the query heads of KV head h of
  * e^(softmax_scale q_i . k_j - lse_i), over the rows that see slot j (`causal` as in
  * kvc_paged_attend, whose q_dev and lse_dev these are; another LSE, e.g. over a window of
- * keys, is as good, where the products q_i . k_j that the row sees are finite or its LSE is
- * not). The sums are fp32, in an order that depends on the sizes alone. A row with an LSE of
- * +inf adds nothing. Errors: as kvc_paged_attend; KVC_ERR_ARG without scores. */
+ * keys, is as good). The sums are fp32, in an order that depends on the sizes alone. A term below
+ * 2^-126 may count as 2^-126; one of 2^128 or more makes the score infinite, one of a product
+ * q_i . k_j that is NaN or +inf infinite or NaN. A row with an LSE of +inf adds nothing.
+ * Errors: as kvc_paged_attend; KVC_ERR_ARG without scores. */
 KVC_API kvc_status kvc_paged_weights(const kvc_paged_batch* batch, const void* q_dev, int64_t q_row_stride,
                                      const float* lse_dev, int32_t rows, const int32_t* row_start_dev,
                                      int32_t causal, void* workspace_dev, int64_t workspace_bytes, void* stream);
