@@ -483,7 +483,7 @@ typedef struct {
   const int32_t* page_table;    /* [num_seqs][max_pages] pages of each sequence's own tokens */
   int32_t* lengths;             /* [num_seqs] tokens that each sequence holds (without the prefix) */
   const int32_t* prefix_pages;  /* [ceil(prefix_tokens / page_size)] or NULL */
-  int32_t* next_positions;      /* [num_seqs] position of the next token appended, or NULL */
+  int32_t* next_positions;      /* [num_seqs] position of the next token appended, or NULL; not `lengths` */
   float* scores;                /* [num_seqs][num_kv_heads][max_pages * page_size] accumulated weight
                                    of the token in each slot, 16-byte aligned, or NULL */
   int32_t* positions;           /* same shape: position of the token in each slot, 16-byte aligned, or NULL */

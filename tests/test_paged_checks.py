@@ -198,3 +198,9 @@ def test_binding_refuses_numbers_past_32_bits():
             with pytest.raises(ValueError, match=name):
                 kvc.kvc_paged_workspace(None, **{**dict(rows=5, keep=64), name: bad})
     kvc._int32(a=-2 ** 31, b=2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_lengths_as_next_positions_refused(no_gpu, name):
+    """An append grows both by its rows: in one array it would add them twice."""
+    assert call(name, batch=dict(next_positions=BATCH["lengths"])) == ARG

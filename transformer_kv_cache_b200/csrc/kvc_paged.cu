@@ -33,6 +33,7 @@ bool valid_batch(const kvc_paged_batch* b) {
   if (b->prefix_tokens < 0 || b->prefix_tokens > kMaxSlots || (b->prefix_tokens > 0 && !b->prefix_pages)) return false;
   if (!(b->softmax_scale > 0.f) || !std::isfinite(b->softmax_scale) || b->reserved != 0) return false;
   if (!b->k_pool || !b->v_pool || !b->page_table || !b->lengths) return false;
+  if (b->next_positions == b->lengths) return false;        // both grow by an append's rows
   return aligned16(b->k_pool) && aligned16(b->v_pool) && aligned16(b->scores) && aligned16(b->positions);
 }
 
