@@ -465,8 +465,9 @@ KVC_API kvc_status kvc_attend_paged_noalloc(const void* q_dev, void* o_dev, cons
  * 16-byte aligned.
  *
  * What the host cannot see is checked on the device: lengths and rows outside their buffers
- * are taken as the nearest that are inside, a page outside the pool is skipped (its keys and
- * values count as zeros; nothing is written to it), and the error word is set. */
+ * are taken as the nearest that are inside (kvc_paged_append takes nothing from such a sequence),
+ * a page outside the pool is skipped (its keys and values count as zeros; nothing is written to
+ * it), and the error word is set. */
 typedef struct {
   int32_t dtype;                /* KVC_F32 or KVC_BF16: Q, K, V, O and the pools */
   int32_t num_seqs;             /* sequences, 1 to 65,535 */
@@ -488,8 +489,8 @@ typedef struct {
                                    of the token in each slot, 16-byte aligned, or NULL */
   int32_t* positions;           /* same shape: position of the token in each slot, 16-byte aligned, or NULL */
   int32_t* error;               /* one word, or NULL: set from 0 by the first device-side failure: 1 a
-                                   bounded wait gave up, 2 no room for an append, 3 a length, row
-                                   or page out of range */
+                                   bounded wait gave up, 2 no room for an append, 3 a length, row,
+                                   page or position out of range */
   float softmax_scale;
   int32_t reserved;             /* must be zero */
 } kvc_paged_batch;
@@ -505,7 +506,8 @@ KVC_API kvc_status kvc_paged_workspace(const kvc_paged_batch* batch, int32_t row
  * in the slots from lengths[b] on; set their scores to 0 and their positions to
  * next_positions[b], next_positions[b] + 1, ... (each where the batch has that array), and
  * clear the rest of a page that is begun. Then lengths[b] and next_positions[b] grow by the
- * sequence's rows. A sequence whose rows do not fit takes none of them (error word 2).
+ * sequence's rows. A sequence whose rows do not fit takes none of them (error word 2), and none
+ * one whose length or rows are out of range or whose next position would pass 2^31 - 1 (3).
  * Errors: KVC_ERR_ARG (batch, pointers, strides; positions without next_positions),
  * KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void* k_dev, const void* v_dev,

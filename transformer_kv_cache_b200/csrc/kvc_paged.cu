@@ -245,13 +245,15 @@ __device__ __forceinline__ void append_task(const AppendParams& p, int b, int lo
     if (p.positions) p.positions[at] = position;
   }
 }
-// A sequence's rows and length; false (and an error) where they are out of range or do not fit.
+// A sequence's rows and length; false (and an error) where they are out of range, would take the next
+// position out of it (2^31 is passed by a day of frames), or do not fit.
 __device__ __forceinline__ bool append_view(const AppendParams& p, int b, int& lo, int& n, int& len) {
   lo = p.row_start[b];
   const int hi = p.row_start[b + 1], cap = p.max_pages << p.page_shift;
   len = p.lengths[b];
   n = hi - lo;
-  const bool in = lo >= 0 && hi >= lo && hi <= p.rows && len >= 0 && len <= cap;
+  const int next = p.next_positions ? p.next_positions[b] : 0;
+  const bool in = lo >= 0 && hi >= lo && hi <= p.rows && len >= 0 && len <= cap && next <= INT_MAX - n;
   if (in && n <= cap - len) return true;
   latch_error(p.err, in ? DERR_POOL : DERR_BOUNDS);
   return false;
