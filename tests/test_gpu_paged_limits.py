@@ -6,8 +6,8 @@ import math
 import pytest
 import torch
 
-from paged_util import Batch, append_ref, weights64
-from test_gpu_paged import DEV, DTYPES, same_state
+from paged_util import Batch, append_ref, attend64, evict_ref, weights64
+from test_gpu_paged import DEV, DTYPES, check_attend, run_attend, same_state, step_tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +69,25 @@ def check_append(kvc, t, error, change=None):
     return c
 
 
+# a few rows a sequence and many, and a batch of one chunk among single rows
+APPENDS = {
+    "a few rows": dict(rows=[1, 0, 8, 5, 3, 7, 2, 16], lengths=[0, 9, 16, 15, 1, 300, 250, 31]),
+    "single rows": dict(rows=[1] * 9, lengths=[0, 1, 15, 16, 17, 63, 64, 255, 256]),
+    "a chunk among single rows": dict(rows=[1] * 30 + [200], lengths=[7 * i for i in range(31)]),
+    "many rows": dict(rows=[40, 0, 17, 90], lengths=[0, 5, 47, 200]),
+    "a row of a frame each": dict(rows=[1] * 700, lengths=[i % 50 for i in range(700)]),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,page,hkv", [(64, 16, 1), (128, 64, 3), (64, 128, 8), (128, 256, 2)])
+@pytest.mark.parametrize("name", APPENDS)
+def test_append_forms(kvc, name, dtype, d, page, hkv):
+    t = Batch(**APPENDS[name], hq=hkv, hkv=hkv, d=d, page=page, dtype=DTYPES[dtype], seed=1, room=200, behind=2)
+    c = check_append(kvc, t, 0)
+    same_state(c, t, name)
+
+
 @pytest.mark.parametrize("rows", [[3, 1, 6, 2], [30, 1, 40, 2]], ids=["a few rows", "many rows"])
 @pytest.mark.parametrize("page", [16, 256])
 def test_append_takes_a_sequence_whole_or_not_at_all(kvc, rows, page):
@@ -105,3 +124,128 @@ def test_append_takes_a_sequence_whole_or_not_at_all(kvc, rows, page):
     t.next_positions[0] = 2 ** 31 - 1 - rows[0]               # the last that fits
     c = check_append(kvc, t, 0)
     same_state(c, t, "last positions")
+
+
+def evict_sorted(t, keep, sinks, recent):
+    """evict_ref for long sequences and scores that are numbers: one sort a head."""
+    slots = torch.arange(t.scores.shape[2])
+    for b in range(t.b):
+        n = int(t.lengths[b])
+        if n <= keep:
+            continue
+        table = t.page_table[b].long()
+        start = int(t.next_positions[b]) - recent
+        for h in range(t.hkv):
+            s, pos = t.scores[b, h, :n], t.positions[b, h, :n]
+            held = (pos < sinks) | (pos >= start)
+            key = torch.where(held, torch.full_like(s, math.inf), s)
+            kept = torch.zeros(n, dtype=torch.bool)
+            kept[torch.sort(key, descending=True, stable=True).indices[:keep]] = True
+            to, frm = slots[:keep][~kept[:keep]], slots[keep:n][kept[keep:]]
+            for pool in (t.k_pool, t.v_pool):
+                pool[table[to // t.page], h, to % t.page] = pool[table[frm // t.page], h, frm % t.page]
+            s[to], pos[to] = s[frm], pos[frm]
+        if keep % t.page:
+            for pool in (t.k_pool, t.v_pool):
+                pool[table[keep // t.page], :, keep % t.page:] = 0
+        t.lengths[b] = keep
+
+
+# one head's slots in a cluster of 1, 2, 4 and 8 CTAs, and all that a cluster of 8 holds
+CLUSTERS = {"1": 8192, "2": 8208, "4": 16400, "8": 32784, "8, full": 393216}
+
+
+@pytest.mark.parametrize("cap", CLUSTERS.values(), ids=CLUSTERS)
+@pytest.mark.parametrize("gone", [1, 8, 9, "half"])
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_evict_in_clusters(kvc, cap, gone, kind):
+    n = cap - 3
+    keep = n // 2 if gone == "half" else n - gone
+    t = Batch(rows=[1], lengths=[n], hq=1, hkv=1, d=64, seed=3, room=3, stale=1.0)
+    assert t.max_pages * t.page == cap
+    g = torch.Generator().manual_seed(4)
+    # ties: few scores, so that runs of equal ones lie in every CTA of the cluster
+    t.scores = torch.exp(3 * torch.randn(t.scores.shape, generator=g)) if kind == "spread" else \
+        torch.randint(0, 3, t.scores.shape, generator=g).float()
+    t.positions[0, 0, :n] = torch.randperm(n + 7, generator=g)[:n].to(torch.int32)
+    t.next_positions += 7
+    u = copy.deepcopy(t)
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    kvc.kvc_paged_evict(batch, keep, 4, 100, c.workspace(kvc, batch, keep))
+    torch.cuda.synchronize()
+    evict_sorted(t, keep, 4, 100)
+    same_state(c, t, cap)
+    assert int(c.error) == 0
+    if cap == 8192 and gone != "half":                        # the sort against the plain reference
+        evict_ref(u, keep, 4, 100)
+        same_state(u, t, "references")
+
+
+def test_pages_cut_inside_serve_the_allocation_free_attention(kvc):
+    """A sequence that an eviction cut and an append continued ends inside a page whose other slots
+    are zeros, in a pool that holds NaN wherever nothing was written: kvc_attend_paged_noalloc, which
+    reads whole pages, gives the same attention."""
+    rows, keep, n = 20, 203, 205
+    t = Batch(rows=[rows], lengths=[230], hq=4, hkv=4, d=64, seed=9, room=40)
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    g = torch.Generator().manual_seed(10)
+    q, k, v = step_tensors(t, g, "cpu")
+    t.q = q
+    start, two = c.row_start.clone(), torch.tensor([0, 2], dtype=torch.int32)
+    work = c.workspace(kvc, batch, keep)
+    kvc.kvc_paged_append(batch, k.to(DEV), v.to(DEV), c.row_start)
+    kvc.kvc_paged_evict(batch, keep, 4, 30, work)
+    kvc.kvc_paged_append(batch, k[:2].to(DEV), v[:2].to(DEV), two.to(DEV))
+    append_ref(t, k, v)
+    evict_ref(t, keep, 4, 30)
+    t.rows, t.row_start = [2], two
+    append_ref(t, k[:2], v[:2])
+    t.rows, t.row_start = [rows], start.cpu()
+    qd = q.to(DEV)
+    o1, lse, o2 = torch.empty_like(qd), torch.empty(q.shape[:2], device=DEV), torch.empty_like(qd)
+    kvc.kvc_paged_attend(batch, qd, o1, start, work, lse=lse, causal=False)
+    table = torch.zeros(-(-n // 16), 4, dtype=torch.int32)
+    table[:, 0] = t.page_table[0, : table.shape[0]]
+    table[:, 3] = 16
+    table[-1, 3] = n % 16
+    kvc.kvc_attend_paged_noalloc(qd, o2, c.k_pool, c.v_pool, c.k_pool.shape[0], table.to(DEV), table.shape[0], rows, 4,
+                                 64, 16, t.scale)
+    torch.cuda.synchronize()
+    same_state(c, t, "state")
+    check_attend(t, False, o1.cpu(), lse.cpu())
+    ref, _, bound, _ = attend64(t, False)
+    # the library's frame attention adds up the weights that it has rounded to bf16, half a step (2^-8)
+    # of each, and its exponential is a cubic of 1.02e-4, in the weights and in their sum: 2^-8 + 2.04e-4 <
+    # 1.06 x 2^-8 of the values' mean magnitude more than `bound`, which holds 2^-8 of it already
+    assert ((o2.cpu().double() - ref).abs() <= 2.06 * bound).all()
+
+
+# one chunk among single rows, in numbers for which the average picks the form that suits neither
+UNEVEN = {
+    "the prefix read by every item": dict(rows=[1] * 15 + [1100], lengths=[40 + 9 * i for i in range(15)] + [1101], hq=8,
+                                          hkv=2, d=64, prefix=333),
+    "the prefix read by every item, 128 dims": dict(rows=[1] * 7 + [530], lengths=[3 + 31 * i for i in range(7)] + [700],
+                                                    hq=4, hkv=1, d=128, page=32, prefix=130),
+    "a chunk in tiles of few rows": dict(rows=[1] * 30 + [180], lengths=[10 * i for i in range(1, 31)] + [500], hq=2,
+                                         hkv=2, d=64, page=64, prefix=77),
+    "a chunk of several tiles": dict(rows=[1] * 10 + [700] + [1] * 10, lengths=[10 * i + 1 for i in range(10)] + [900] +
+                                     [300] * 10, hq=2, hkv=1, d=128, prefix=0),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", UNEVEN)
+def test_a_chunk_among_single_rows(kvc, name, dtype):
+    t = Batch(**UNEVEN[name], dtype=DTYPES[dtype], seed=5, behind=3)
+    for causal in (True, False):
+        o, lse = run_attend(kvc, t, causal)
+        check_attend(t, causal, o, lse)
+        c = copy.deepcopy(t).to(DEV)
+        batch = c.handle(kvc)
+        kvc.kvc_paged_weights(batch, c.q, lse.to(DEV), c.row_start, c.workspace(kvc, batch), causal=causal)
+        torch.cuda.synchronize()
+        assert int(c.error) == 0
+        ref, bound = weights64(t, lse, causal)
+        assert ((c.scores.cpu().double() - ref).abs() <= bound).all()
