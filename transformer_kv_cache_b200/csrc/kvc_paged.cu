@@ -632,6 +632,8 @@ extern "C" kvc_status kvc_paged_evict(const kvc_paged_batch* batch, int32_t keep
   const long long cap = static_cast<long long>(batch->max_pages) * batch->page_size;
   if (cap <= keep) return KVC_OK;              // no sequence can be longer
   if (cap > paged_evict_max_slots()) return KVC_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms < 1) return KVC_ERR_CUDA;
   EvictParams p{};
   p.B = batch->num_seqs;
   p.Hkv = batch->num_kv_heads;
@@ -653,5 +655,5 @@ extern "C" kvc_status kvc_paged_evict(const kvc_paged_batch* batch, int32_t keep
   p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace_dev) + evict_counts_bytes(batch));
   p.move_cap = move_cap(batch, keep);
   p.err = batch->error;
-  return status_of(launch_paged_evict(static_cast<cudaStream_t>(stream), p, batch->lengths));
+  return status_of(launch_paged_evict(static_cast<cudaStream_t>(stream), p, sms, batch->lengths));
 }

@@ -538,6 +538,6 @@ struct EvictParams {
   int* err;
 };
 int paged_evict_max_slots();
-cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int32_t* lengths);
+cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int sms, int32_t* lengths);
 
 }  // namespace kvc

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
 
 int paged_evict_max_slots() { return kMaxCluster * kMaxChunk; }
 
-cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int32_t* lengths) {
+cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int sms, int32_t* lengths) {
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(paged_evict_select_kernel),
@@ -433,7 +433,7 @@ cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int32_t* le
   const int cap = p.max_pages << p.page_shift;
   int ranks = 1;
   while (ranks < kMaxCluster &&
-         (cap > ranks * kMaxChunk || (cap > ranks * kSlots && static_cast<long long>(p.B) * p.Hkv * ranks < 148)))
+         (cap > ranks * kMaxChunk || (cap > ranks * kSlots && static_cast<long long>(p.B) * p.Hkv * ranks < sms)))
     ranks *= 2;
   const int chunk = (((cap + ranks - 1) / ranks) + 31) & ~31;
   cudaLaunchConfig_t cfg{};
