@@ -12,7 +12,13 @@ namespace kvc {
 namespace {
 
 constexpr int kMaxGroup = 64;                  // query heads per KV head
-constexpr int kFewRows = 8;                    // rows a sequence (on average) up to which a CTA appends them
+// A CTA appends a sequence's rows in one launch up to kFewRows a sequence, on average, and kFewBytes of K
+// and V in all, since one sequence may have nearly all of them, which one SM then copies at some 40 GB/s. Against
+// the form of two launches (rows of 4 KB): 64 sequences' single rows 5.2 for 7.1 us, their 8 rows 6.1 for 7.8; one
+// of 193 rows beside 63 single ones 27 for 7.7, and above the limit one of 449 52 for 7.8, 1,024 single rows 13.1
+// for 9.0 (though 256 sequences' 8 rows 7.7 for 10.3).
+constexpr int kFewRows = 8;
+constexpr long long kFewBytes = 1 << 20;
 constexpr int kManyHeads = 8192;               // rows x heads from which on the merge packs four into a warp
 constexpr long long kMaxSlots = 1LL << 29;     // slots of a sequence, tokens of the prefix: their sum is an int
 
@@ -551,8 +557,8 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void*
   p.positions = batch->positions;
   p.err = batch->error;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // few rows a sequence: one launch, a CTA for each
-  if (rows <= kFewRows * p.B) return status_of(launch_pdl(paged_append_few_kernel, dim3(p.B), dim3(512), 0, s, p));
+  if (rows <= kFewRows * p.B && 2LL * rows * p.H * p.row_bytes <= kFewBytes)
+    return status_of(launch_pdl(paged_append_few_kernel, dim3(p.B), dim3(512), 0, s, p));
   const long long warps = rows + static_cast<long long>(p.B) * (batch->page_size - 1);
   if (warps > INT_MAX - 8) return KVC_ERR_ARG;
   cudaError_t e = launch_pdl(paged_append_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, p);
