@@ -12,11 +12,10 @@
 // two tiles a stream is a tile; an item of one tile (a decode step's few rows) gives its key tiles
 // to the streams by turns, each with a maximum and sum of its own.
 //
-// With D = 64 the exponentials are the bound and TMEM has room: a stream's keys are halved, 64 of a
-// tile to each of two softmax warpgroups with an accumulator O, maximum and sum of their own,
-// which are joined through shared memory at the end of a segment. Four warps a scheduler then
-// cover one another's waits (two, with S double-buffered instead: 586 TFLOP/s over 73,292 keys).
-// With D = 128 the two accumulators fill TMEM, and a softmax warpgroup takes all 128 keys.
+// A stream's softmax is one warpgroup, a row to a thread, for 64 dims as for 128. (With 64 dims TMEM has
+// room for two accumulators a stream, each with half of the keys: four warps a scheduler, a quarter of the
+// exponentials on the FMA pipe, but 96 registers a thread, 7 stages for 10 and a join at a segment's end.
+// Slower throughout: 1,004 rows over 73,292 keys 457 us for 442, 64 sequences of 130 rows 291 for 258.)
 //
 // Roles: warp 3 walks the schedule and hands out its segments through a ring in shared memory,
 // some segments ahead (the walk's loads and divisions are off everybody else's path), and loads the
@@ -55,21 +54,16 @@ using namespace paged;
 constexpr int kTile = 128;                     // query rows of a tile, keys of a unit
 constexpr float kGrow = 8.0f;                  // a weight above 2^8 moves the row's reference maximum
 constexpr int kAhead = 3;                      // segments handed out before their queries are loaded
+constexpr int kSoftWarps = 8;                  // four to a stream
+constexpr int kThreads = 128 + 32 * kSoftWarps;
+constexpr int kRegsLow = 88, kRegsHigh = 208;  // of warps 0 to 3 and of the softmax: in all 168 a thread, as at launch
 
-template <int D, int SUB>
+template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;                       // 128-byte swizzled blocks of a row
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : SUB == 1 ? 10 : 7;
-  static constexpr int kSub = SUB;                             // softmax warpgroups of a stream
-  static constexpr int kCols = kTile / kSub;                   // keys of a tile for each
-  static constexpr int kSoftWarps = 8 * kSub;
-  static constexpr int kThreads = 128 + 32 * kSoftWarps;
-  // registers of warps 0 to 3 and of the softmax warps: in all those at launch, 168 or 96 a thread
-  static constexpr int kRegsLow = SUB == 1 ? 88 : 64, kRegsHigh = SUB == 1 ? 208 : 104;
-  static constexpr int kPoly8 = SUB == 1 ? 0 : 2;              // of 8 pairs, the exponentials on the FMA pipe
-  static constexpr int kJoinBytes = kSub == 2 ? 2 * kTile * (D * 4 + 8) : 0;
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kJoinBytes + 1216;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 1216;
 };
 
 struct Bars {
@@ -77,7 +71,6 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];              // query slots
   uint64_t s_full[2], p_full[2];
   uint64_t o_full[2], o_free[2];
-  uint64_t x_full[2], x_empty[2];              // the second warpgroup's results in shared memory
   uint64_t tail_full[10];                      // tiles of V that end inside a box, before full
   uint64_t drained;
   SegmentRing ring;
@@ -98,16 +91,16 @@ __device__ __forceinline__ int stream_tile(const Segment& g, int w, int u) {
 // The ring holds the tiles of a segment of n in the order in which the streams use them: K0, K1 V0,
 // K2 V1, ..., V(n-1). The entry of V(t):
 __device__ __forceinline__ int v_entry(int t, int n) { return t + 1 == n ? 2 * n - 1 : 2 * t + 2; }
-// Weights of one row's step: P = 2^(s c - m) as bf16 pairs, returning their sum (before the
-// rounding). kPoly of every 8 pairs go to the FMA pipe, the others to the MUFU, spread through the
-// row. Masked steps hold -inf and use the MUFU alone, which gives exact zeros.
-template <int kPoly>
+// Weights of one row's step: P = 2^(s c - m) as bf16 pairs, returning their sum before the rounding, which
+// the log-sum-exp keeps in full. The tensor core takes 16-bit weights, and bf16 ones need no scaling; a
+// rounding is half a step (2^-8) at most, of each weight apart, so that over a row they mostly cancel: the
+// outputs, rounded to bf16 themselves, are 1.7e-3 from the exact ones where fp32 weights give 1.66e-3.
 __device__ __forceinline__ float weigh(const uint32_t* s, uint64_t c2, uint64_t nm2, uint32_t (&pb)[32]) {
   uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     const uint64_t x = fma2_pair(s[2 * k], s[2 * k + 1], c2, nm2);
-    const uint64_t e = (k & 7) >= 8 - kPoly ? exp2_pair(x) : exp2_pair_mufu(x);
+    const uint64_t e = exp2_pair_mufu(x);
     if (k & 1) sum1 = add2(sum1, e);
     else sum0 = add2(sum0, e);
     float e0, e1;
@@ -137,18 +130,16 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {
 // Whether a tile with `valid` keys before the sequence's end has its last inside a box of blk slots.
 __device__ __forceinline__ bool ends_inside(int valid, int blk) { return valid < kTile && (valid & (blk - 1)); }
 
-template <int D, int SUB>
-__global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
     paged_attend_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PagedParams p) {
-  using C = Cfg<D, SUB>;
+  using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                     // [slot][half][128 rows][128 B]
   uint8_t* kv_s = q_s + 2 * C::kTileBytes;                 // [stage][8 keys][half][key][128 B]
-  float4* join_o = reinterpret_cast<float4*>(kv_s + C::kStages * C::kTileBytes);    // [stream][4 dims][128 rows]
-  float2* join_ml = reinterpret_cast<float2*>(join_o + (C::kSub == 2 ? 2 * kTile * D / 4 : 0));   // [stream][128 rows]
-  Bars& bar = *reinterpret_cast<Bars*>(join_ml + (C::kSub == 2 ? 2 * kTile : 0));
+  Bars& bar = *reinterpret_cast<Bars*>(kv_s + C::kStages * C::kTileBytes);
   static_assert(sizeof(Bars) <= 1216, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bar.abort;
@@ -163,14 +154,12 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4 * C::kSub);
+      mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.o_free[i], 4 * C::kSub);
-      mbar_init(&bar.x_full[i], 4);
-      mbar_init(&bar.x_empty[i], 4);
+      mbar_init(&bar.o_free[i], 4);
     }
     mbar_init(&bar.drained, 1);
-    ring_init(bar.ring, 3 + C::kSoftWarps);    // warps 0, 1, 2 and the softmax
+    ring_init(bar.ring, 3 + kSoftWarps);    // warps 0, 1, 2 and the softmax
     bar.abort = 0;
     mbar_fence_init();
   }
@@ -187,12 +176,11 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
   if (warp == 3 || !plan_by_warp(p))
     walk = plan_walk(p, bar.plan, [&](int b, const SeqView& v) { return head_units(p, b, v); });
   const uint32_t tmem = bar.tmem;
-  // TMEM columns: S of stream w at 128 w, the weights of its warpgroup j at 128 w + 64 j, their O at
-  // 256 + (w * kSub + j) * D
+  // TMEM columns: S of stream w at 128 w, overwritten by its weights, O at 256 + w D
   const int blk = min(1 << p.page_shift, kTile);           // slots of a box
 
   if (warp == 0) {
-    reg_dealloc<C::kRegsLow>();
+    reg_dealloc<kRegsLow>();
     // ------------------------------------------------------------------ K and V
     if (lane == 0) {
       tma_prefetch_desc(&tmap_k);
@@ -274,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       for (int i = max(0, e - C::kStages); i < e; ++i)
         wait_drain(&bar.full[i % C::kStages], (i / C::kStages) & 1, abort);
   } else if (warp == 3) {
-    reg_dealloc<C::kRegsLow>();
+    reg_dealloc<kRegsLow>();
     // ------------------------------------------------------------------ schedule and queries
     if (lane == 0) {
       tma_prefetch_desc(&tmap_q);
@@ -313,7 +301,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         if (used[i]) wait_drain(&bar.q_full[i], (used[i] - 1) & 1, abort);
     }
   } else if (warp == 1) {
-    reg_dealloc<C::kRegsLow>();
+    reg_dealloc<kRegsLow>();
     // ------------------------------------------------------------------ products
     const uint32_t idesc_s = idesc_f16kind(1, kTile, kTile, 0, 0);
     const uint32_t idesc_o = idesc_f16kind(1, kTile, D, 0, 1);
@@ -349,11 +337,9 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     auto add_v = [&](int w, int u, int stage) {            // O += P V
       const uint64_t vd = v_desc + (stage * C::kTileBytes >> 4);
 #pragma unroll
-      for (int j = 0; j < C::kSub; ++j)
-#pragma unroll
-        for (int c = 0; c < C::kCols / 16; ++c)
-          mma_ts(tmem + 256 + (w * C::kSub + j) * D, tmem + w * 128 + j * 64 + c * 8,
-                 vd + ((j * C::kCols + c * 16) * (D * 2) >> 4), idesc_o, u > 0 || c > 0 ? 1u : 0u);
+      for (int c = 0; c < kTile / 16; ++c)
+        mma_ts(tmem + 256 + w * D, tmem + w * 128 + c * 8, vd + (c * 16 * (D * 2) >> 4), idesc_o,
+               u > 0 || c > 0 ? 1u : 0u);
     };
 #pragma unroll 1
     for (int sg = 0;; ++sg) {
@@ -460,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
     __syncwarp();
     wait_drain(&bar.drained, 0, abort);
   } else if (warp == 2) {
-    reg_dealloc<C::kRegsLow>();
+    reg_dealloc<kRegsLow>();
     // ------------------------------------------------------------------ the last values of a sequence
     // What the cache holds behind a length must not meet a weight of 0 (0 x NaN): zeros to V's rows
     // behind the last token, up to the end of its box, then the tile is handed on.
@@ -498,12 +484,12 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       e0 += 2 * (g.k1 - g.k0);
     }
   } else {
-    reg_alloc<C::kRegsHigh>();
-    // ------------------------------------------------------------------ softmax: stream w, keys j of a tile
-    const int group = (warp - 4) >> 2, w = group / C::kSub, j = group % C::kSub, wq = warp & 3;
+    reg_alloc<kRegsHigh>();
+    // ------------------------------------------------------------------ softmax of stream w
+    const int w = (warp - 4) >> 2, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + w * 128 + j * 64;
-    const uint32_t o_col = tmem + lane_base + 256 + group * D;
+    const uint32_t s_col = tmem + lane_base + w * 128;
+    const uint32_t o_col = tmem + lane_base + 256 + w * D;
     const float c = p.scale_log2;
     const int r = wq * 32 + lane, r_tok = r / p.G, r_head = r - r_tok * p.G;   // row, its token and head
     int done = 0, segs = 0;
@@ -537,17 +523,17 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          uint32_t s[C::kCols];
+          uint32_t s[kTile];
 #pragma unroll
-          for (int q = 0; q < C::kCols / 32; ++q)
+          for (int q = 0; q < kTile / 32; ++q)
             tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
           const int tile = first + u * stride;
-          const int valid = (tile < prefix_tiles(p) ? p.prefix_tokens : limit) - tile * kTile - j * C::kCols;
-          const bool masked = __any_sync(0xffffffffu, valid < C::kCols);
+          const int valid = (tile < prefix_tiles(p) ? p.prefix_tokens : limit) - tile * kTile;
+          const bool masked = __any_sync(0xffffffffu, valid < kTile);
           tmem_ld_wait();
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < C::kCols; ++k)
+            for (int k = 0; k < kTile; ++k)
               if (k >= valid) s[k] = 0xff800000u;
           }
           // the row's reference maximum moves when a weight would pass 2^8, or on a NaN
@@ -574,8 +560,8 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           const uint64_t c2 = pk2(c, c), nm2 = pk2(-base, -base);
           uint32_t pb[32];
 #pragma unroll
-          for (int q = 0; q < C::kCols / 64; ++q) {
-            l += C::kPoly8 > 0 && masked ? weigh<0>(&s[64 * q], c2, nm2, pb) : weigh<C::kPoly8>(&s[64 * q], c2, nm2, pb);
+          for (int q = 0; q < kTile / 64; ++q) {
+            l += weigh(&s[64 * q], c2, nm2, pb);
             tmem_st32(s_col + 32 * q, pb);
           }
           tmem_st_wait();
@@ -599,32 +585,14 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ring.empty[sg % kRing]);
       if (steps == 0) {
-        if (j == 0 && mine) p.part_ml[slot] = make_float2(m, l);
+        if (mine) p.part_ml[slot] = make_float2(m, l);
         continue;
       }
       ok = wait_near(&bar.o_full[w], segs & 1, abort);
-      // the second warpgroup's results go to the first through shared memory
-      if (C::kSub == 2 && j == 1 && segs > 0)
-        ok = ok && wait_near(&bar.x_empty[w], (segs - 1) & 1, abort);
-      if (C::kSub == 2 && j == 0) ok = ok && wait_near(&bar.x_full[w], segs & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      float4* mate = join_o + w * (kTile * D / 4) + r;
-      float own = 1.f, other = 0.f;            // factors of the two warpgroups' results
-      if (C::kSub == 2) {
-        if (j == 1) {
-          join_ml[w * kTile + r] = make_float2(m, l);
-        } else {
-          const float2 ml = join_ml[w * kTile + r];
-          const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
-          own = ex2(m - base);
-          other = ex2(ml.x - base);
-          l = l * own + ml.y * other;
-          m = top;
-        }
-      }
-      if (j == 0 && mine) {
+      if (mine) {
         if (!whole) p.part_ml[slot] = make_float2(m, l);
         else if (p.lse) p.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
       }
@@ -655,33 +623,13 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
           uint32_t o[32];
           tmem_ld32(o_col + 32 * q, o);
           tmem_ld_wait();
-          if (C::kSub == 2 && j == 1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mate[(8 * q + k) * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                      __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-          } else {
-            if (C::kSub == 2) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 x = mate[(8 * q + k) * kTile];
-                o[4 * k] = __float_as_uint(__uint_as_float(o[4 * k]) * own + x.x * other);
-                o[4 * k + 1] = __float_as_uint(__uint_as_float(o[4 * k + 1]) * own + x.y * other);
-                o[4 * k + 2] = __float_as_uint(__uint_as_float(o[4 * k + 2]) * own + x.z * other);
-                o[4 * k + 3] = __float_as_uint(__uint_as_float(o[4 * k + 3]) * own + x.w * other);
-              }
-            }
-            if (mine) store(o, q);
-          }
+          if (mine) store(o, q);
           __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (C::kSub == 2) mbar_arrive(j == 1 ? &bar.x_full[w] : &bar.x_empty[w]);
-        mbar_arrive(&bar.o_free[w]);
-      }
+      if (lane == 0) mbar_arrive(&bar.o_free[w]);
       ++segs;
     }
   }
@@ -694,22 +642,22 @@ __global__ void __launch_bounds__(Cfg<D, SUB>::kThreads, 1)
   }
 }
 
-template <int D, int SUB>
+template <int D>
 cudaError_t launch(cudaStream_t s, const PagedParams& p, const CUtensorMap& q, const CUtensorMap& k,
                    const CUtensorMap& v) {
-  using C = Cfg<D, SUB>;
+  using C = Cfg<D>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    const void* kernel = reinterpret_cast<const void*>(paged_attend_tc_kernel<D, SUB>);
+    const void* kernel = reinterpret_cast<const void*>(paged_attend_tc_kernel<D>);
     // the warps' shares come out of what the block is launched with; a larger sum would wait forever
     cudaFuncAttributes at;
     if (const cudaError_t got = cudaFuncGetAttributes(&at, kernel); got != cudaSuccess) return got;
-    if (at.numRegs * C::kThreads < 32 * (4 * C::kRegsLow + C::kSoftWarps * C::kRegsHigh))
+    if (at.numRegs * kThreads < 32 * (4 * kRegsLow + kSoftWarps * kRegsHigh))
       return cudaErrorLaunchOutOfResources;
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   return e != cudaSuccess ? e
-                          : launch_pdl(paged_attend_tc_kernel<D, SUB>, dim3(p.grid), dim3(C::kThreads), C::kSmem, s, q,
+                          : launch_pdl(paged_attend_tc_kernel<D>, dim3(p.grid), dim3(kThreads), C::kSmem, s, q,
                                        k, v, p);
 }
 
@@ -719,10 +667,7 @@ cudaError_t launch_paged_attend_tc(cudaStream_t s, const PagedParams& p) {
   CUtensorMap q, k, v;
   if (!encode_rows_tmap(&q, p.q, p) || !encode_slots_tmap(&k, p.k_pool, p) || !encode_slots_tmap(&v, p.v_pool, p))
     return cudaErrorInvalidValue;
-  if (p.D == 128) return launch<128, 1>(s, p, q, k, v);
-  // the sequences' rows fill more than a tile, on average
-  const bool many = p.rows > static_cast<long long>(p.B) * p.tile_tokens;
-  return many ? launch<64, 2>(s, p, q, k, v) : launch<64, 1>(s, p, q, k, v);
+  return p.D == 64 ? launch<64>(s, p, q, k, v) : launch<128>(s, p, q, k, v);
 }
 
 }  // namespace kvc

@@ -27,22 +27,16 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-// 2^x of a pair on the FMA pipe: x is clamped below at -126 and split as n + f, n = rint(x)
+// 2^x of a pair on the FMA pipe: x is clamped to [-126, 128] and split as n + f, n = rint(x)
 // (the 1.5 * 2^23 shift), f in [-0.5, 0.5]; 2^f is a quartic with p(0) = 1, fitted by iteratively
 // reweighted least squares on the relative error (at most 2.9e-6 in fp32, 3.4e-7 on average);
-// n goes into the exponent field. x must stay below 127.5, or is clamped at 128 too (kTop), where the
-// exponent field gives +inf, as every larger x and a NaN do then: no term that passes fp32, and none of a
-// product that is no number, comes out finite. (A clamp at 127, which costs the same, made 2^127 of them.)
-template <bool kTop = false>
+// n goes into the exponent field. At 128 that gives +inf, as every larger x and a NaN do then: no term that
+// passes fp32, and none of a product that is no number, comes out finite.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x2) {
   constexpr float kShift = 12582912.0f;
   float x0, x1;
   up2(x2, x0, x1);
-  if (kTop) {
-    x0 = fminf(x0, 128.f);
-    x1 = fminf(x1, 128.f);
-  }
-  const uint64_t xc = pk2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t xc = pk2(fmaxf(fminf(x0, 128.f), -126.f), fmaxf(fminf(x1, 128.f), -126.f));
   const uint64_t t = add2(xc, pk2(kShift, kShift));
   const uint64_t n = add2(t, pk2(-kShift, -kShift));
   const uint64_t f = fma2(n, pk2(-1.f, -1.f), xc);

@@ -88,8 +88,8 @@ __device__ __forceinline__ void add_all(const uint32_t (&s)[32], const float* y,
     const float4 v = *reinterpret_cast<const float4*>(y + 2 * k);
     const uint64_t x0 = fma2(pk2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, pk2(v.x, v.y));
     const uint64_t x1 = fma2(pk2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])), c2, pk2(v.z, v.w));
-    sum0 = add2(sum0, (k & 7) >= 8 - kPoly8 ? exp2_pair<true>(x0) : exp2_pair_mufu(x0));
-    sum1 = add2(sum1, ((k + 1) & 7) >= 8 - kPoly8 ? exp2_pair<true>(x1) : exp2_pair_mufu(x1));
+    sum0 = add2(sum0, (k & 7) >= 8 - kPoly8 ? exp2_pair(x0) : exp2_pair_mufu(x0));
+    sum1 = add2(sum1, ((k + 1) & 7) >= 8 - kPoly8 ? exp2_pair(x1) : exp2_pair_mufu(x1));
   }
 }
 
