@@ -249,3 +249,70 @@ def test_a_chunk_among_single_rows(kvc, name, dtype):
         assert int(c.error) == 0
         ref, bound = weights64(t, lse, causal)
         assert ((c.scores.cpu().double() - ref).abs() <= bound).all()
+
+
+def in_guarded_memory(t):
+    """The batch on the device with its pools, scores and positions as parts of one buffer, between bytes
+    of 0x5a; and what gives the bytes that no array has."""
+    names = ("k_pool", "v_pool", "scores", "positions")
+    c = copy.deepcopy(t)
+    at, gap = {}, 1 << 16
+    end = gap
+    for name in names:
+        x = getattr(c, name)
+        at[name] = end
+        end += (x.numel() * x.element_size() + 255) // 256 * 256 + gap
+    buf = torch.full((end,), 0x5a, dtype=torch.uint8, device=DEV)
+    free = torch.ones(end, dtype=torch.bool, device=DEV)
+    views = {}
+    for name in names:
+        x = getattr(c, name)
+        n = x.numel() * x.element_size()
+        views[name] = buf[at[name]:at[name] + n].view(x.dtype).view(x.shape)
+        views[name].copy_(x)
+        free[at[name]:at[name] + n] = False
+        setattr(c, name, torch.empty(0))
+    c.to(DEV)
+    for name in names:
+        setattr(c, name, views[name])
+    return c, lambda: buf[free]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_workspace_shared_by_mistake_stays_a_mistake_of_numbers(kvc, dtype):
+    """Two batches of different sizes whose calls run at the same time with one workspace, which the
+    header forbids: their numbers may be wrong, but nothing outside of their arrays is touched."""
+    small = Batch(rows=[3, 1, 200], lengths=[700, 900, 1000], hq=4, hkv=2, d=64, prefix=100, dtype=DTYPES[dtype], seed=1,
+                  stale=0.0)
+    large = Batch(rows=[1, 2] * 20 + [300], lengths=[400 + 50 * i for i in range(40)] + [3000], hq=8, hkv=8, d=64, page=32,
+                  dtype=DTYPES[dtype], seed=2, stale=0.0)
+    keep = 150
+    calls, works = [], []
+    for t in (small, large):
+        c, outside = in_guarded_memory(t)
+        b = c.handle(kvc)
+        works.append(c.workspace(kvc, b, keep))
+        calls.append((c, b, outside, c.lengths.clone(), c.scores.clone(), torch.empty_like(c.q),
+                      torch.empty(c.q.shape[:2], device=DEV), torch.cuda.Stream()))
+    work = max(works, key=lambda w: w.numel())
+    torch.cuda.synchronize()
+    for i in range(60):
+        for c, b, _, lengths, scores, o, lse, s in calls if i % 2 else calls[::-1]:
+            with torch.cuda.stream(s):
+                c.lengths.copy_(lengths)
+                c.scores.copy_(scores)
+                kvc.kvc_paged_attend(b, c.q, o, c.row_start, work, lse=lse)
+                kvc.kvc_paged_weights(b, c.q, lse, c.row_start, work)
+                kvc.kvc_paged_evict(b, keep, 4, 16, work)
+    torch.cuda.synchronize()
+    for c, _, outside, *_ in calls:
+        assert (outside() == 0x5a).all()
+        assert c.lengths.tolist() == [keep] * c.b
+    # and with a workspace each the same arrays still give what they should
+    for (c, b, _, lengths, scores, o, lse, _), w, t in zip(calls, works, (small, large)):
+        c.lengths.copy_(lengths)
+        for name in ("k_pool", "v_pool"):
+            getattr(c, name).copy_(getattr(t, name))
+        kvc.kvc_paged_attend(b, c.q, o, c.row_start, w, lse=lse, causal=True)
+        torch.cuda.synchronize()
+        check_attend(t, True, o.cpu(), lse.cpu())

@@ -348,7 +348,9 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   griddep_wait();
   griddep_launch_dependents();
   if (b < 0) return;                                   // behind the last sequence: left as it was
-  const long long U = __ldcg(p.plan), own = __ldcg(p.plan + 1 + b);
+  // (a call that wrongly runs beside another with the same workspace merges other partials, but reads
+  // none outside of it: the CTAs are bounded)
+  const long long U = max(__ldcg(p.plan), 1LL), own = __ldcg(p.plan + 1 + b);
   // the partials in the order of their keys: per part its CTAs' pieces, per piece its streams
   int c = 0, n = 0;
   if (nk > 0) {
@@ -357,9 +359,9 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       end = c;
-      c = static_cast<int>(quotient(k == 0 ? u0 + nk - 1 : u0, U));
+      c = static_cast<int>(min(quotient(max(k == 0 ? u0 + nk - 1 : u0, 0LL), U), p.grid - 1LL));
     }
-    const int pieces = end - c + 1;
+    const int pieces = max(end - c, 0) + 1;
     n = pieces == 1 && whole ? -1 : pieces << (place & 1);
   }
   const int c0 = __shfl_sync(0xffffffffu, c, 0, LANES), c1 = __shfl_sync(0xffffffffu, c, LANES / 2, LANES);
@@ -454,7 +456,11 @@ __global__ void __launch_bounds__(256) paged_weights_merge_kernel(const PagedPar
   griddep_launch_dependents();
   const int c = blockIdx.x;
   const int4 id = p.part_id[c];
-  if (!id.w) return;
+  // what a concurrent call may have left in a workspace that it wrongly shares is no place outside the scores
+  auto within = [](int x, int n) { return static_cast<unsigned>(x) < static_cast<unsigned>(n); };
+  if (!id.w || !within(id.x, p.B) || !within(id.y, p.Hkv) ||
+      !within(id.z, (paged_cap(p) + p.key_tile - 1) >> p.key_shift))
+    return;
   auto same = [&](int k) {
     if (k < 0 || k >= p.grid) return false;
     const int4 o = p.part_id[k];

@@ -348,16 +348,21 @@ __global__ void __launch_bounds__(kThreads, 4) paged_evict_select_kernel(const E
 
 // Moves [per_cta x, + per_cta) of (sequence z, head y). The first CTA of a head also clears the slots
 // behind the last kept one, to the end of its page: they are the lowest slots that moves can come
-// from, so that those moves, if any, are among its own.
+// from, so that those moves, if any, are among its own. What comes from the workspace is bounded again: a
+// call that wrongly runs beside another with the same workspace moves the wrong tokens, but none elsewhere.
 __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const EvictParams p, int32_t* lengths, int per_cta) {
   griddep_wait();
   griddep_launch_dependents();
   const int t = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const long long bh = static_cast<long long>(b) * p.Hkv + h;
-  const int moves = p.counts[bh];
+  const int moves = min(p.counts[bh], p.move_cap);
   const int first = blockIdx.x * per_cta;
   if (moves < 0 || (first >= moves && first > 0)) return;
   const int cap = p.max_pages << p.page_shift;
+  const int pool_rows = static_cast<int>((p.pool_pages * p.Hkv) << p.page_shift);
+  auto sound = [&](int2 at) {
+    return static_cast<unsigned>(at.x) < static_cast<unsigned>(cap) && at.y < pool_rows ? at : make_int2(-1, -1);
+  };
   float* scores = p.scores + bh * cap;
   int32_t* positions = p.positions + bh * cap;
   const int2* list_to = p.moves + bh * 2 * p.move_cap;
@@ -374,8 +379,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = r + u * per;
-      src[u] = i < end ? list_from[i] : make_int2(-1, -1);
-      dst[u] = i < end ? list_to[i] : make_int2(-1, -1);
+      src[u] = i < end ? sound(list_from[i]) : make_int2(-1, -1);
+      dst[u] = i < end ? sound(list_to[i]) : make_int2(-1, -1);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
         *reinterpret_cast<uint4*>(p.k_pool + c) = k[u];
         *reinterpret_cast<uint4*>(p.v_pool + c) = v[u];
       }
-      if (src[u].x >= 0 && part == 0) {
+      if (src[u].x >= 0 && dst[u].x >= 0 && part == 0) {
         scores[dst[u].x] = scores[src[u].x];
         positions[dst[u].x] = positions[src[u].x];
       }
