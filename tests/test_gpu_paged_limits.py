@@ -316,3 +316,129 @@ def test_a_workspace_shared_by_mistake_stays_a_mistake_of_numbers(kvc, dtype):
         kvc.kvc_paged_attend(b, c.q, o, c.row_start, w, lse=lse, causal=True)
         torch.cuda.synchronize()
         check_attend(t, True, o.cpu(), lse.cpu())
+
+
+def test_workspace_serves_fewer_rows(kvc):
+    """The workspace for some rows is enough for every smaller number, and one that is too small is
+    refused."""
+    for dtype in DTYPES:
+        for b, hq, hkv, d, prefix in ((1, 1, 1, 64, 0), (7, 8, 2, 64, 100), (64, 32, 8, 128, 5), (3, 64, 1, 128, 1000)):
+            t = Batch(rows=[1] * b, lengths=[20] * b, hq=hq, hkv=hkv, d=d, prefix=prefix, dtype=DTYPES[dtype], seed=1).to(DEV)
+            batch = t.handle(kvc)
+            sizes = [kvc.kvc_paged_workspace(batch, n) for n in list(range(1200)) + [4096, 8191, 8192]]
+            assert sizes == sorted(sizes)
+        o, lse = torch.empty_like(t.q), torch.empty(t.q.shape[:2], device=DEV)
+        small = torch.empty(256, dtype=torch.uint8, device=DEV)
+        for call in (lambda: kvc.kvc_paged_attend(batch, t.q, o, t.row_start, small, lse=lse),
+                     lambda: kvc.kvc_paged_weights(batch, t.q, lse, t.row_start, small),
+                     lambda: kvc.kvc_paged_evict(batch, 8, 0, 0, small)):
+            with pytest.raises(kvc.KVCError):
+                call()
+        torch.cuda.synchronize()
+        assert int(t.error) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_graph_replays_follow_rows_and_tables(kvc, dtype):
+    """A captured attention and its weights, replayed for other row starts (none at all among them), other
+    lengths and other pages."""
+    t = Batch(rows=[100, 20, 24], lengths=[300, 90, 700], hq=4, hkv=2, d=64, prefix=70, dtype=DTYPES[dtype], seed=3)
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    work = c.workspace(kvc, batch)
+    o, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device=DEV)
+
+    def step():
+        kvc.kvc_paged_attend(batch, c.q, o, c.row_start, work, lse=lse)
+        kvc.kvc_paged_weights(batch, c.q, lse, c.row_start, work)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rows, lengths, swap in (([100, 20, 24], [300, 90, 700], False), ([1, 1, 1], [300, 90, 700], True),
+                                ([0, 0, 0], [300, 90, 700], False), ([0, 144, 0], [300, 50, 0], False),
+                                ([140, 0, 3], [1, 0, 700], True)):
+        u = copy.deepcopy(t)
+        u.rows, u.lengths = rows, torch.tensor(lengths, dtype=torch.int32)
+        u.row_start = torch.tensor([0] + torch.tensor(rows).cumsum(0).tolist(), dtype=torch.int32)
+        if swap:                                              # the first sequence's tokens in other pages
+            n = -(-300 // 16)
+            new = t.page_table[2, torch.arange(n) + 44 - n].flip(0).clone()      # of the third's last ones
+            u.k_pool[new.long()], u.v_pool[new.long()] = (p[t.page_table[0, :n].long()] for p in (t.k_pool, t.v_pool))
+            u.page_table[0, :n] = new
+            u.lengths[2] = min(int(u.lengths[2]), (44 - n) * 16)
+        for name in ("lengths", "row_start", "page_table", "k_pool", "v_pool", "scores"):
+            getattr(c, name).copy_(getattr(u, name))
+        o.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(c.error) == 0
+        check_attend(u, True, o.cpu(), lse.cpu())
+        ref, bound = weights64(u, lse.cpu(), True)
+        assert ((c.scores.cpu().double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_as_many_sequences_as_there_may_be(kvc, dtype):
+    """65,535 sequences of up to 40 tokens, a row each: append, attention, weights, eviction."""
+    b, d, keep = 65535, 64, 20
+    dt = DTYPES[dtype]
+    g = torch.Generator(device=DEV).manual_seed(1)
+    normal = lambda *s: torch.randn(s, generator=g, device=DEV).to(dt)
+    k_pool, v_pool = normal(b * 3, 1, 16, d), normal(b * 3, 1, 16, d)
+    table = torch.randperm(b * 3, generator=g, device=DEV).to(torch.int32).view(b, 3)
+    lengths = (torch.arange(b, device=DEV) % 40).to(torch.int32)
+    after = lengths.clone()
+    scores, positions = torch.zeros(b, 1, 48, device=DEV), torch.arange(48, device=DEV).to(torch.int32).expand(b, 1, -1).contiguous()
+    error = torch.zeros(1, dtype=torch.int32, device=DEV)
+    batch = kvc.make_paged_batch(k_pool, v_pool, table, lengths, 1, d ** -0.5, next_positions=after, scores=scores,
+                                 positions=positions, error=error)
+    rows = torch.arange(b + 1, device=DEV).to(torch.int32)
+    q, k, v = normal(b, 1, d), normal(b, 1, d), normal(b, 1, d)
+    work = torch.empty(kvc.kvc_paged_workspace(batch, b, keep), dtype=torch.uint8, device=DEV)
+    o, lse = torch.empty_like(q), torch.empty(b, 1, device=DEV)
+    kvc.kvc_paged_append(batch, k, v, rows)
+    kvc.kvc_paged_attend(batch, q, o, rows, work, lse=lse)
+    kvc.kvc_paged_weights(batch, q, lse, rows, work)
+    torch.cuda.synchronize()
+    n = (torch.arange(b, device=DEV) % 40) + 1
+    assert int(error) == 0 and torch.equal(lengths, n.to(torch.int32)) and torch.equal(after, lengths)
+    own = lambda pool: pool[table.long(), 0].reshape(b, 48, d)
+    at = torch.arange(b, device=DEV)
+    assert torch.equal(own(k_pool)[at, n - 1], k[:, 0]) and torch.equal(own(v_pool)[at, n - 1], v[:, 0])
+    there = torch.arange(48, device=DEV).view(1, -1) < n.view(-1, 1)
+    keys, values, q64 = own(k_pool).double(), own(v_pool).double(), q.double()
+    zero = torch.zeros((), dtype=torch.float64, device=DEV)
+    x = torch.where(there, (keys * q64).sum(-1) * d ** -0.5, zero - math.inf)
+    a = torch.where(there, (keys * q64).abs().sum(-1) * d ** -0.5, zero)
+    w = torch.softmax(x, -1)
+    # the bounds of attend64 and weights64
+    u, half = 2.0 ** -24, torch.finfo(dt).eps / 2
+    slack = 4 * (d + 2) * u * a.amax(-1, keepdim=True)
+    e = torch.expm1(2 * slack) + 2.0 ** -21 + 96 * u
+    ref, mass = (w.unsqueeze(-1) * values).sum(1), (w.unsqueeze(-1) * values.abs()).sum(1)
+    bound = (2 * e + (half if dt != torch.float32 else 0)) * mass * 1.01 + half * ref.abs() * 1.01
+    assert ((o[:, 0].double() - ref).abs() <= bound).all()
+    assert ((lse.double() - torch.logsumexp(x, -1, keepdim=True)).abs() <=
+            2 * slack + e + 4 * u * lse.double().abs() + 2.0 ** -21).all()
+    y = lse.double()
+    grow = torch.where(there, torch.exp(x - y), zero)
+    slack = 4 * (d + 2) * u * a + 4 * u * (y.abs() + a)
+    limit = grow * (torch.expm1(2 * slack) + 2.0 ** -21 + 6 * u) + 4 * u * grow
+    assert ((scores[:, 0].double() - grow).abs() <= limit).all()
+    # eviction: the kept tokens' scores, and every token with the key and value that it came with
+    held, k_old = scores[:, 0].clone(), own(k_pool).clone()
+    kvc.kvc_paged_evict(batch, keep, 2, 5, work)
+    torch.cuda.synchronize()
+    assert int(error) == 0 and torch.equal(lengths, n.clamp(max=keep).to(torch.int32))
+    cut = (n > keep).nonzero().view(-1)
+    pos = torch.arange(48, device=DEV).view(1, -1)
+    key = torch.where((pos < 2) | (pos >= (n - 5).view(-1, 1)), torch.full_like(held, math.inf), held)
+    key = torch.where(there, key, torch.full_like(held, -1.0))[cut]
+    best = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :keep]
+    kept = positions[cut, 0, :keep].long()
+    assert torch.equal(kept.sort(1).values, best.sort(1).values)
+    assert torch.equal(scores[cut, 0, :keep], held[cut].gather(1, kept))
+    assert torch.equal(own(k_pool)[cut, :keep], k_old[cut].gather(1, kept.unsqueeze(-1).expand(-1, -1, d)))
