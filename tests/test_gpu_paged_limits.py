@@ -442,3 +442,21 @@ def test_as_many_sequences_as_there_may_be(kvc, dtype):
     assert torch.equal(kept.sort(1).values, best.sort(1).values)
     assert torch.equal(scores[cut, 0, :keep], held[cut].gather(1, kept))
     assert torch.equal(own(k_pool)[cut, :keep], k_old[cut].gather(1, kept.unsqueeze(-1).expand(-1, -1, d)))
+
+
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 64, 16), ("f32", 128, 32)])
+def test_evict_many_heads(kvc, dtype, d, page):
+    """So many heads that a CTA takes all of a head's moves, with room for many more tokens."""
+    b, hkv, keep = 310, 8, 105
+    t = Batch(rows=[1] * b, lengths=[keep + i for i in range(b)], hq=hkv, hkv=hkv, d=d, page=page, dtype=DTYPES[dtype],
+              seed=3, stale=1.0, room=100)
+    g = torch.Generator().manual_seed(4)
+    t.scores = torch.randint(0, 50, t.scores.shape, generator=g).float()
+    t.next_positions += 3
+    c = copy.deepcopy(t).to(DEV)
+    batch = c.handle(kvc)
+    kvc.kvc_paged_evict(batch, keep, 4, 10, c.workspace(kvc, batch, keep))
+    torch.cuda.synchronize()
+    evict_sorted(t, keep, 4, 10)
+    same_state(c, t, "many heads")
+    assert int(c.error) == 0

@@ -23,6 +23,9 @@
 // Moves. Bound by memory (two rows read and written each). The selection looks the pages up, so
 // that a move is two dependent loads, its entry in the list and its rows, and a thread has kUnroll
 // moves under way.
+// The keys' shared memory is laid out for what a sequence has room for, since no length is known on the
+// host: room for 32,768 tokens leaves an SM one CTA of the selection, and 64 of 4,160 tokens go in 74 us where
+// room for 4,160 takes 22 (64 sequences of 8 heads).
 //
 // 64 sequences of 8 heads of 4,097 tokens, one of which goes: 14 us a step with the append, most of it
 // the three launches' own. 4 sequences of up to 32,768 tokens cut to 4,096: 49 us (120 MB: 2.4 TB/s),
@@ -42,6 +45,7 @@ constexpr int kBins = 2048;
 constexpr int kFew = 8;                        // evicted tokens that are taken one by one
 constexpr int kMoveThreads = 256;
 constexpr int kMoves = 32;                     // moves of a CTA, or the slots of a page where those are more
+constexpr int kMoveCtas = 16;                  // of an SM, at most
 constexpr int kSlots = 8192;                   // slots from which on a (sequence, head) gets another CTA
 constexpr int kUnroll = 2;
 
@@ -346,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 4) paged_evict_select_kernel(const E
   if (t == 0 && rank == 0) p.counts[bh] = static_cast<int>(moves);
 }
 
-// Moves [per_cta x, + per_cta) of (sequence z, head y). The first CTA of a head also clears the slots
-// behind the last kept one, to the end of its page: they are the lowest slots that moves can come
-// from, so that those moves, if any, are among its own. What comes from the workspace is bounded again: a
+// Moves [per_cta x, + per_cta) of (sequence z, head y), and so on by the grid. The first CTA of a head also
+// clears the slots behind the last kept one, to the end of its page: they are the lowest slots that moves
+// can come from, so that those moves, if any, are among its first. What comes from the workspace is bounded again: a
 // call that wrongly runs beside another with the same workspace moves the wrong tokens, but none elsewhere.
 __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const EvictParams p, int32_t* lengths, int per_cta) {
   griddep_wait();
@@ -356,8 +360,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
   const int t = threadIdx.x, h = blockIdx.y, b = blockIdx.z;
   const long long bh = static_cast<long long>(b) * p.Hkv + h;
   const int moves = min(p.counts[bh], p.move_cap);
-  const int first = blockIdx.x * per_cta;
-  if (moves < 0 || (first >= moves && first > 0)) return;
+  const int stride = static_cast<int>(gridDim.x) * per_cta;
+  if (moves < 0) return;
   const int cap = p.max_pages << p.page_shift;
   const int pool_rows = static_cast<int>((p.pool_pages * p.Hkv) << p.page_shift);
   auto sound = [&](int2 at) {
@@ -372,37 +376,39 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
   const int lanes = p.row_bytes >> 4;                      // lanes of a row: 8, 16 or 32
   const int per = kMoveThreads / lanes;                    // rows a CTA moves at once
   const int part = (t % lanes) * 16;
-  const int end = min(moves, first + per_cta);
-  for (int r = first + t / lanes; r < end; r += kUnroll * per) {
-    int2 src[kUnroll], dst[kUnroll];
-    uint4 k[kUnroll], v[kUnroll];
+  for (int first = blockIdx.x * per_cta; first < moves; first += stride) {
+    const int end = min(moves, first + per_cta);
+    for (int r = first + t / lanes; r < end; r += kUnroll * per) {
+      int2 src[kUnroll], dst[kUnroll];
+      uint4 k[kUnroll], v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = r + u * per;
-      src[u] = i < end ? sound(list_from[i]) : make_int2(-1, -1);
-      dst[u] = i < end ? sound(list_to[i]) : make_int2(-1, -1);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (src[u].y >= 0 && dst[u].y >= 0) {
-        const long long a = static_cast<long long>(src[u].y) * p.row_bytes + part;
-        k[u] = *reinterpret_cast<const uint4*>(p.k_pool + a);
-        v[u] = *reinterpret_cast<const uint4*>(p.v_pool + a);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = r + u * per;
+        src[u] = i < end ? sound(list_from[i]) : make_int2(-1, -1);
+        dst[u] = i < end ? sound(list_to[i]) : make_int2(-1, -1);
       }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (src[u].y >= 0 && dst[u].y >= 0) {
-        const long long c = static_cast<long long>(dst[u].y) * p.row_bytes + part;
-        *reinterpret_cast<uint4*>(p.k_pool + c) = k[u];
-        *reinterpret_cast<uint4*>(p.v_pool + c) = v[u];
-      }
-      if (src[u].x >= 0 && dst[u].x >= 0 && part == 0) {
-        scores[dst[u].x] = scores[src[u].x];
-        positions[dst[u].x] = positions[src[u].x];
+      for (int u = 0; u < kUnroll; ++u)
+        if (src[u].y >= 0 && dst[u].y >= 0) {
+          const long long a = static_cast<long long>(src[u].y) * p.row_bytes + part;
+          k[u] = *reinterpret_cast<const uint4*>(p.k_pool + a);
+          v[u] = *reinterpret_cast<const uint4*>(p.v_pool + a);
+        }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (src[u].y >= 0 && dst[u].y >= 0) {
+          const long long c = static_cast<long long>(dst[u].y) * p.row_bytes + part;
+          *reinterpret_cast<uint4*>(p.k_pool + c) = k[u];
+          *reinterpret_cast<uint4*>(p.v_pool + c) = v[u];
+        }
+        if (src[u].x >= 0 && dst[u].x >= 0 && part == 0) {
+          scores[dst[u].x] = scores[src[u].x];
+          positions[dst[u].x] = positions[src[u].x];
+        }
       }
     }
   }
-  if (first > 0) return;
+  if (blockIdx.x > 0) return;
   if (t == 0 && h == 0) lengths[b] = p.keep;
   if (p.keep & page_mask) {
     __syncthreads();
@@ -458,8 +464,14 @@ cudaError_t launch_paged_evict(cudaStream_t s, const EvictParams& p, int sms, in
   e = cudaLaunchKernelEx(&cfg, paged_evict_select_kernel, p, chunk);
   if (e != cudaSuccess) return e;
   const int per_cta = std::max(kMoves, 1 << p.page_shift);
-  return launch_pdl(paged_evict_move_kernel, dim3((p.move_cap + per_cta - 1) / per_cta, p.Hkv, p.B), dim3(kMoveThreads),
-                    0, s, p, lengths, per_cta);
+  // A CTA for per_cta moves where all that the sequences have room for need no more than kMoveCtas an SM;
+  // else that many, which then run through the moves. Without the limit a token a step of 64 sequences of
+  // 8 heads, kept 4,096 with room for as many, takes 76 us, 73 of them for CTAs that find no move; with it
+  // 11.5 (9.9 at 4 an SM, which cut 16 sequences from 12,000 tokens to 6,000 in 135 us, 16 in 107).
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  const int ctas = static_cast<int>(std::min<long long>((p.move_cap + per_cta - 1) / per_cta,
+                                                        (static_cast<long long>(kMoveCtas) * sms + heads - 1) / heads));
+  return launch_pdl(paged_evict_move_kernel, dim3(ctas, p.Hkv, p.B), dim3(kMoveThreads), 0, s, p, lengths, per_cta);
 }
 
 }  // namespace kvc
