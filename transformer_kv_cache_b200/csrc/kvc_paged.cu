@@ -14,9 +14,9 @@ namespace {
 constexpr int kMaxGroup = 64;                  // query heads per KV head
 // A CTA appends a sequence's rows in one launch up to kFewRows a sequence, on average, and kFewBytes of K
 // and V in all, since one sequence may have nearly all of them, which one SM then copies at some 40 GB/s. Against
-// the form of two launches (rows of 4 KB): 64 sequences' single rows 5.2 for 7.1 us, their 8 rows 6.1 for 7.8; one
-// of 193 rows beside 63 single ones 27 for 7.7, and above the limit one of 449 52 for 7.8, 1,024 single rows 13.1
-// for 9.0 (though 256 sequences' 8 rows 7.7 for 10.3).
+// the form of two launches (rows of 4 KB; 2.5 us of each are copies that reset the lengths): 64 sequences'
+// single rows 4.7 for 6.5 us, their 8 rows 5.8 for 7.5; one of 193 rows beside 63 single ones 25 for 7.4, and
+// above the limit one of 449 49 for 7.2, 1,024 single rows 11.5 for 8.7 (though 256 sequences' 8 rows 6.7 for 10.1).
 constexpr int kFewRows = 8;
 constexpr long long kFewBytes = 1 << 20;
 constexpr int kManyHeads = 8192;               // rows x heads from which on the merge packs four into a warp
@@ -211,19 +211,21 @@ struct AppendParams {
   float* scores;
   int32_t* positions;
   int* err;
+  int behind_warps;                                   // of a sequence, for the slots behind its last token
 };
 
-// One task of a sequence (a warp): task i < n copies its i-th row, the tasks behind those clear the
-// slots behind its last token, where the call begins that page (every page of the cache ends in
-// zeros). 16 bytes a lane.
+// Slots to clear behind a sequence's last token, where the call begins that page (every page of the
+// cache ends in zeros).
+__device__ __forceinline__ int append_behind(const AppendParams& p, int n, int len) {
+  const int page_size = 1 << p.page_shift, end = len + n, first = end & ~(page_size - 1);
+  return n == 0 || end == first || first < len ? 0 : first + page_size - end;
+}
+// One task of a sequence (a warp): task i < n copies its i-th row, the tasks behind those clear a
+// slot behind its last token each. 16 bytes a lane.
 __device__ __forceinline__ void append_task(const AppendParams& p, int b, int lo, int n, int len, int task) {
   const int lane = threadIdx.x & 31, page_size = 1 << p.page_shift;
   const bool copy = task < n;
-  int slot = len + task;
-  if (!copy) {
-    const int end = len + n, first = end & ~(page_size - 1);   // first slot of the last page written
-    if (n == 0 || end == first || first < len || slot >= first + page_size) return;
-  }
+  const int slot = len + task;
   const int32_t page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + (slot >> p.page_shift));
   if (page < 0 || page >= p.pool_pages) {
     if (lane == 0) latch_error(p.err, DERR_BOUNDS);
@@ -277,25 +279,30 @@ __global__ void __launch_bounds__(512) paged_append_few_kernel(const AppendParam
   const int b = blockIdx.x, warps = blockDim.x >> 5;
   int lo, n, len;
   if (!append_view(p, b, lo, n, len)) return;
-  const int tasks = n + (1 << p.page_shift) - 1;
+  const int tasks = n + append_behind(p, n, len);
   for (int task = threadIdx.x >> 5; task < tasks; task += warps) append_task(p, b, lo, n, len, task);
   __syncthreads();
   if (threadIdx.x == 0) grow(p, b, n, len);
 }
 
-// A warp per row of the batch and per slot that may need clearing; the lengths grow in a kernel of
+// A warp per row of the batch, and `behind_warps` a sequence for the slots behind its last token; the lengths grow in a kernel of
 // their own, once nobody reads the old ones. 2 x 1,004 rows of 16 heads of 64 dims (16 MB): 8 us, half
 // of them the two launches.
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), behind = (1 << p.page_shift) - 1;
+  const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int z = warp - p.rows;
-  const int b = z < 0 ? find_sequence(p.row_start, p.B, warp) : z / behind;
+  const int b = z < 0 ? find_sequence(p.row_start, p.B, warp) : z / p.behind_warps;
   if (b < 0 || b >= p.B) return;                       // behind the last sequence
   int lo, n, len;
   if (!append_view(p, b, lo, n, len)) return;
-  append_task(p, b, lo, n, len, z < 0 ? warp - lo : n + z % behind);
+  if (z < 0) {
+    append_task(p, b, lo, n, len, warp - lo);
+    return;
+  }
+  const int behind = append_behind(p, n, len);
+  for (int i = z % p.behind_warps; i < behind; i += p.behind_warps) append_task(p, b, lo, n, len, n + i);
 }
 __global__ void paged_grow_kernel(const AppendParams p) {
   griddep_wait();
@@ -565,7 +572,11 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows <= kFewRows * p.B && 2LL * rows * p.H * p.row_bytes <= kFewBytes)
     return status_of(launch_pdl(paged_append_few_kernel, dim3(p.B), dim3(512), 0, s, p));
-  const long long warps = rows + static_cast<long long>(p.B) * (batch->page_size - 1);
+  // One for each slot that a page may need cleared, in all up to 4,096 and never fewer than a page of 16
+  // needs: 1,024 sequences' single rows in pages of 256 take 8.8 us, with a warp for every slot 41; 8
+  // sequences' 512 rows 11.8, with 15 warps a sequence 15.5.
+  p.behind_warps = std::min(batch->page_size - 1, std::max(15, 4096 / p.B));
+  const long long warps = rows + static_cast<long long>(p.B) * p.behind_warps;
   if (warps > INT_MAX - 8) return KVC_ERR_ARG;
   cudaError_t e = launch_pdl(paged_append_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, p);
   if (e == cudaSuccess) e = launch_pdl(paged_grow_kernel, dim3((p.B + 255) / 256), dim3(256), 0, s, p);
