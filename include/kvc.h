@@ -455,13 +455,14 @@ KVC_API kvc_status kvc_attend_paged_noalloc(const void* q_dev, void* o_dev, cons
  * Pages are laid out as kvc_append_frame writes them, [page][KV head][slot][dim], and a
  * sequence's page that kvc_paged_append began or kvc_paged_evict cut ends in zeros, so the
  * pages can be given to kvc_attend_paged_noalloc (16-slot pages, 64 dims, bf16, as many
- * query heads as KV heads). No page may be in two sequences' rows of the page table, or in
+ * query heads as KV heads; a caller that lowers a length by itself clears the slots behind it
+ * before that, which the calls below never use). No page may be in two sequences' rows of the page table, or in
  * the prefix and a row, if it is appended to or evicted from.
  *
  * Query head i reads KV head i / (num_q_heads / num_kv_heads). Rows of Q, K and V are the
  * sequences' tokens one after another: row_start_dev[b] <= row < row_start_dev[b + 1] are
- * sequence b's; rows outside [row_start_dev[0], row_start_dev[num_seqs]) are neither read nor
- * written. Row strides are in elements (a slice of a fused QKV tensor can be given), rows
+ * sequence b's; rows outside [row_start_dev[0], row_start_dev[num_seqs]) are left as they are and
+ * change no result, whatever they hold (they may be read). Row strides are in elements (a slice of a fused QKV tensor can be given), rows
  * 16-byte aligned.
  *
  * What the host cannot see is checked on the device: lengths and rows outside their buffers
@@ -520,7 +521,9 @@ KVC_API kvc_status kvc_paged_append(const kvc_paged_batch* batch, const void* k_
  * causal = 1 the rows are the sequence's last n tokens (appended before the call): row i of n
  * sees the prefix and the slots up to lengths[b] - n + i; with 0 it sees every slot. A row
  * that sees nothing gets O = 0 and an LSE of -inf. The prefix's keys and values are read for
- * the whole batch at once. o_dev is densely packed. bf16 runs on tcgen05 tensor cores (fp32
+ * the whole batch at once; where it has 256 rows or more a sequence on average, each counted once per
+ * query head of a KV head (64 in fp32), each sequence's rows read them before its own keys.
+ * o_dev is densely packed. bf16 runs on tcgen05 tensor cores (fp32
  * logits, statistics and accumulation, weights rounded to bf16 for the second product), fp32
  * in fp32 arithmetic. Logits are to stay below 2^20 in magnitude, as for kvc_attend. A key
  * that is no number makes the rows that see it NaN; a value that is none can reach every row

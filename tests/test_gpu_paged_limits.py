@@ -460,3 +460,32 @@ def test_evict_many_heads(kvc, dtype, d, page):
     evict_sorted(t, keep, 4, 10)
     same_state(c, t, "many heads")
     assert int(c.error) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_behind_the_last_sequence_change_nothing(kvc, dtype):
+    """Rows of a padded batch hold NaN and infinities: every result is the same, bit for bit."""
+    base = dict(rows=[3, 0, 150, 1], lengths=[40, 7, 333, 129], hq=4, hkv=2, d=64, prefix=50, room=160, behind=200)
+    runs = []
+    for value in (0.0, math.nan, math.inf):
+        t = Batch(**base, dtype=DTYPES[dtype], seed=6)
+        total = int(t.row_start[-1])
+        t.q[total:] = value
+        c = copy.deepcopy(t).to(DEV)
+        batch = c.handle(kvc)
+        work = c.workspace(kvc, batch, 30)
+        k, v = (x.clone() for x in append_inputs(t))
+        k[total:], v[total:] = value, value
+        o, lse = torch.full(c.q.shape, 7.0, dtype=t.dtype, device=DEV), torch.full(c.q.shape[:2], 7.0, device=DEV)
+        lse[total:] = value
+        kvc.kvc_paged_append(batch, k.to(DEV), v.to(DEV), c.row_start)
+        kvc.kvc_paged_attend(batch, c.q, o, c.row_start, work, lse=lse)
+        kvc.kvc_paged_weights(batch, c.q, lse, c.row_start, work)
+        kvc.kvc_paged_evict(batch, 30, 2, 5, work)
+        torch.cuda.synchronize()
+        assert int(c.error) == 0 and (o[total:] == 7).all()
+        runs.append([x.cpu() for x in (o[:total], lse[:total], c.scores, c.positions, c.lengths,
+                                       c.k_pool.view(torch.uint8), c.v_pool.view(torch.uint8))])
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            assert torch.equal(a, b)

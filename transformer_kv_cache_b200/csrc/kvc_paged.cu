@@ -99,7 +99,11 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   p->prefix_units = (b->prefix_tokens + (b->dtype == KVC_BF16 ? 128 : 64) - 1) / (b->dtype == KVC_BF16 ? 128 : 64);
   // Where the sequences' rows fill their items (on average), packing the batch's rows saves no
   // pass over the prefix: each item then reads the prefix before its own keys, and its rows'
-  // partials need no joining with those of a second item.
+  // partials need no joining with those of a second item. No sequence's rows are known here, so that in a
+  // mixed batch the others read the prefix for themselves too; B of them at most, beside a chunk of
+  // about B items that read it anyway. 32 heads on 8 of 128 dims behind 16,384 tokens, joined and not: 64
+  // sequences of 64 rows 1,040 us and 1,366, 15 single rows and one of 1,100 480 and 504, 63 and one of
+  // 4,100 1,668 and 1,356.
   if (b->dtype == KVC_BF16) {
     // two tiles of 128 packed rows share a CTA's key tiles
     p->tile_tokens = 128 / p->G;
@@ -118,7 +122,8 @@ void attend_schedule(PagedParams* p, const kvc_paged_batch* b) {
   // Tiles of 16 query rows where a sequence has no more (a 64-row tile of them would spend its
   // products on padding), else of 64. The prefix's of 16 up to two of them (8 sequences' row of 4 heads
   // each behind 1,500 tokens: 22.5 us, in one tile of 64 26), of 64 from there on (at 31 tokens 29 us, in
-  // tiles of 16 33).
+  // tiles of 16 33). A chunk among single rows is faster in the small tiles as well (63 rows of one and one of 900:
+  // 237 us, in tiles of 64 309).
   const long long all = static_cast<long long>(p->rows) * p->G;
   const int few = p->G <= 16 && (all + p->B - 1) / p->B <= 16 ? 16 : 64;
   const int prefix = few == 16 && all <= 32 ? 16 : 64;
@@ -142,7 +147,7 @@ void weights_schedule(PagedParams* p, const kvc_paged_batch* b) {
     return;
   }
   // tiles of 32 rows, of which only fours that there are cost anything, where a sequence has no more
-  // (16 sequences of 4 rows of 6 heads: 82 us, in tiles of 64 120; of 4 heads' one row: 76, in 16 72)
+  // (16 sequences of 4 rows of 6 heads: 82 us, in tiles of 64 120; of 4 heads' one row: 75, in 16 72)
   const long long per_seq = (static_cast<long long>(p->rows) + p->B - 1) / p->B * p->G;
   p->tile_tokens = p->item_tokens = (per_seq <= 32 ? 32 : 64) / p->G;
   p->key_tile = 64;
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(512) paged_append_few_kernel(const AppendParam
 }
 
 // A warp per row of the batch, and `behind_warps` a sequence for the slots behind its last token; the lengths grow in a kernel of
-// their own, once nobody reads the old ones. 2 x 1,004 rows of 16 heads of 64 dims (16 MB): 8 us, half
+// their own, once nobody reads the old ones. 2 x 1,004 rows of 16 heads of 64 dims (16 MB): 6 us, half
 // of them the two launches.
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   griddep_wait();

@@ -114,7 +114,8 @@ __device__ __forceinline__ bool two_tiles(const PagedParams& p, const SeqView& v
 __device__ __forceinline__ int tile_cost(const PagedParams& p, const SeqView& v, int i) {
   return two_tiles(p, v, i) ? p.cost_two : p.cost_one;
 }
-// sum over j < n of floor((a j + b) / m), for a, b >= 0: whole multiples of m come out in closed
+// sum over j < n of floor((a j + b) / m), for a, b >= 0, by the known Euclid-like floor sum: whole
+// multiples of m come out in closed
 // form, and the rest counts lattice points under a line, which is the same sum with a and m
 // exchanged and fewer terms (the steps of Euclid's algorithm on a and m).
 // Every value stays below 2^32: rows and keys of a sequence do.

@@ -30,16 +30,18 @@
 //
 // Slots past a sequence's length are never used: boxes past it are loaded from behind the
 // pool's end, which TMA fills with zeros, warp 2 clears the last box of V behind the last token
-// (the loading warp copying that box instead held up all loads: 90 for 58 us at 64 sequences of 512
+// (the loading warp copying that box instead held up all loads: 90 for 55 us at 64 sequences of 512
 // to 1,024 tokens in pages of 128 slots), and those keys' scores are set to -inf whatever K held.
 //
 // What bounds it. Few rows: the bytes of K and V (32 sequences of 4,096 to 8,192 tokens, 8 KV heads
-// of 128 dims: 139 us, 5.8 TB/s), and where sequences are short a segment's end and start, some 1 us,
-// and the call's own, some 12 us (64 of 512 to 1,024: 50 us). Both come from beyond the instruction cache, so
+// of 128 dims: 133 us, 6.1 TB/s), and where sequences are short a segment's end and start, some 1 us,
+// and the call's own, some 12 us (64 of 512 to 1,024: 51 us). Both come from beyond the instruction cache, so
 // the code is kept small (121 KB of it took 64 us there, 90 KB 50). Many rows, 128 dims: S = Q K^T
 // reads both operands from shared memory, 8 KB for 64 cycles of the tensor core, all that it gives
-// (4,096 rows over 16,384 keys: 249 us, 1,104 TFLOP/s); 64 dims: the exponentials (2 sequences'
-// 1,004 rows of 16 heads over 8,032 shared keys and 4,016 and 8,032 of their own: 199 us, 583 TFLOP/s).
+// (4,096 rows of 8 heads over 16,384 keys: 245 us, 1,122 TFLOP/s); 64 dims: no pipe, but a stream's chain of
+// product, score load, maximum, exponentials and weight store, which two warps a scheduler cover in part
+// (MUFU 57 % of its peak, issue slots 34 %, tensor core 29 %; 2 sequences' 1,004 rows of 16 heads over 8,032
+// shared keys and 4,016 and 8,032 of their own: 191 us, 606 TFLOP/s).
 //
 // Every barrier wait is bounded; a role that gives up sets the error word, and the CTA drains
 // its copies and products, frees its TMEM and returns.
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.o_free[i], 4);
     }
     mbar_init(&bar.drained, 1);
-    ring_init(bar.ring, 3 + kSoftWarps);    // warps 0, 1, 2 and the softmax
+    ring_init(bar.ring, 3 + kSoftWarps);       // warps 0, 1, 2 and the softmax
     bar.abort = 0;
     mbar_fence_init();
   }

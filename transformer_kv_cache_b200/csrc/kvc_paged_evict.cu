@@ -28,7 +28,7 @@
 // room for 4,160 takes 22 (64 sequences of 8 heads).
 //
 // 64 sequences of 8 heads of 4,097 tokens, one of which goes: 14 us a step with the append, most of it
-// the three launches' own. 4 sequences of up to 32,768 tokens cut to 4,096: 49 us (120 MB: 2.4 TB/s),
+// the three launches' own. 4 sequences of up to 32,768 tokens cut to 4,096: 51 us (120 MB: 2.4 TB/s),
 // a third of it the selection, three passes whose barriers a cluster of four waits for.
 #include <algorithm>
 

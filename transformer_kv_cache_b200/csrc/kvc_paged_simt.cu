@@ -8,10 +8,10 @@
 //
 // What shared memory gives back (512 bytes in four cycles for a load of 16 bytes a lane) bounds the
 // products: 64 rows are 4 x 4 of them to a thread, 16 x 16 threads, eight loads for 64 FFMA, twice the
-// FFMAs' own time (300 rows over 4,000 tokens, weights: 21 TFLOP/s with 64 dims, 25 with 128). Few
-// rows are dealt out so that no thread computes rows that there are not: 16 sequences of 2,048
-// to 4,096 tokens, 8 heads of 64 dims: attention 56 us, 3.6 TB/s (128 as 16 x 16 threads), the weights
-// with 128 dims 70 us, 2.9 TB/s (247).
+// FFMAs' own time (300 rows over 4,000 tokens: attention 26 TFLOP/s with 64 dims, 29 with 128, weights 21
+// and 25). Few rows are dealt out so that no thread computes rows that there are not: 16 sequences of 2,048
+// to 4,096 tokens, 8 heads of 64 dims: attention 59 us, 3.4 TB/s (128 as 16 x 16 threads), the weights
+// with 128 dims 74 us, 2.8 TB/s (247).
 #include <math_constants.h>
 
 #include "kvc_paged.cuh"
