@@ -456,14 +456,14 @@ KVC_API kvc_status kvc_attend_paged_noalloc(const void* q_dev, void* o_dev, cons
  * sequence's page that kvc_paged_append began or kvc_paged_evict cut ends in zeros, so the
  * pages can be given to kvc_attend_paged_noalloc (16-slot pages, 64 dims, bf16, as many
  * query heads as KV heads; a caller that lowers a length by itself clears the slots behind it
- * before that, which the calls below never use). No page may be in two sequences' rows of the page table, or in
- * the prefix and a row, if it is appended to or evicted from.
+ * before that, which the calls below never use). No page may be in two sequences' rows of the
+ * page table, or in the prefix and a row, if it is appended to or evicted from.
  *
  * Query head i reads KV head i / (num_q_heads / num_kv_heads). Rows of Q, K and V are the
  * sequences' tokens one after another: row_start_dev[b] <= row < row_start_dev[b + 1] are
  * sequence b's; rows outside [row_start_dev[0], row_start_dev[num_seqs]) are left as they are and
- * change no result, whatever they hold (they may be read). Row strides are in elements (a slice of a fused QKV tensor can be given), rows
- * 16-byte aligned.
+ * change no result, whatever they hold (they may be read). Row strides are in elements (a slice
+ * of a fused QKV tensor can be given), rows 16-byte aligned.
  *
  * What the host cannot see is checked on the device: lengths and rows outside their buffers
  * are taken as the nearest that are inside (kvc_paged_append takes nothing from such a sequence),

@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(512) paged_append_few_kernel(const AppendParam
   if (threadIdx.x == 0) grow(p, b, n, len);
 }
 
-// A warp per row of the batch, and `behind_warps` a sequence for the slots behind its last token; the lengths grow in a kernel of
-// their own, once nobody reads the old ones. 2 x 1,004 rows of 16 heads of 64 dims (16 MB): 6 us, half
+// A warp per row of the batch, and `behind_warps` a sequence for the slots behind its last token; the
+// lengths grow in a kernel of their own, once nobody reads the old ones. 2 x 1,004 rows of 16 heads of 64 dims (16 MB): 6 us, half
 // of them the two launches.
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   griddep_wait();
